@@ -16,6 +16,7 @@ LIB_PATH = os.path.join(HERE, "libmoe_fp8.so")
 _p = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
+_l = ctypes.c_longlong
 _z = ctypes.c_size_t
 
 # name -> (restype, argtypes), in the order of include/moe_fp8.h
@@ -53,6 +54,12 @@ SIGNATURES = {
     "moe_combine": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _p, _p]),
     "moe_combine_fp32": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _p, _p]),
     "moe_bias_update": (_i, [_p, _p, _i, _i, _i, _f, _p, _p]),
+    "moe_rmsnorm_quant": (_i, [_p, _l, _p, _i, _p, _i, _f, _i, _i, _p, _p, _p, _p, _p]),
+    "moe_rmsnorm_backward_workspace": (_z, [_i, _i]),
+    "moe_rmsnorm_backward": (_i, [_p, _p, _i, _p, _i, _f, _p, _i, _i, _p, _p, _p, _z, _p]),
+    "moe_few_tokens_workspace": (_z, [_i, _i, _i, _i, _i]),
+    "moe_few_tokens": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _i,
+                            _p, _p, _p, _p, _p, _z, _p]),
     "moe_debug_wait_timeout": (_i, [_i, _p]),
 }
 

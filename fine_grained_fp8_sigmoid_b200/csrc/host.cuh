@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 #include <cstdio>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 

@@ -8,3 +8,5 @@
 #include "combine.cu"
 #include "ep.cu"
 #include "backward.cu"
+#include "norm.cu"
+#include "few.cu"

@@ -456,6 +456,102 @@ MOE_API int moe_bias_update(float* b, const int32_t* counts, int N_r, int T, int
                     float gamma, float* max_over_mean_out, void* stream);
 
 /*
+ * ---------------------------------------------------------------- pre-norm
+ * moe_rmsnorm_quant: root-mean-square norm before the layer, with the
+ * residual's addition and the experts' E4M3 input:
+ *   s = x + res,  h = s,  y = s / sqrt(mean(s^2) + eps) * w
+ * The pages show the layer from u_t on; the norm that makes u_t has no
+ * counterpart on them (its 1x128 output does: "DeepSeek-V3 Teknik Raporu",
+ * Temel fikirler, FP8 bullet).
+ *   x      [rows][d] bf16, rows ldx elements apart (ldx >= d, a multiple of 8)
+ *   res    NULL (s = x), or the residual stream [rows][d], bf16, or FP32 when
+ *          stream_is_fp32
+ *   w      [d] FP32, or bf16 when w_is_bf16
+ *   h      NULL, or [rows][d] (out): the stream after the addition, of res's type
+ *   y      NULL, or [rows][d] bf16 (out): the router's input u
+ *   q, scale  both NULL, or [rows][d] E4M3 and [rows][d/128] FP32 (out): y in
+ *          1x128 tiles, by moe_quant_1x128's rule
+ * Everything between the inputs and each output's one rounding is FP32: y and
+ * q are formed from the unrounded s, and q from the unrounded y. At least one
+ * of h, y, q is wanted. h may alias res (or x, if ldx = d and the stream is
+ * bf16), and y may alias x (if ldx = d). A row whose s^2 overflows FP32 gives
+ * y = 0, as the FP32 formula does; NaN and infinities stay in their row.
+ * Limits: d a multiple of 8, of 128 with q, and at most 32768.
+ */
+MOE_API int moe_rmsnorm_quant(const uint16_t* x, long long ldx, const void* res,
+                      int stream_is_fp32, const void* w, int w_is_bf16, float eps,
+                      int rows, int d, void* h, uint16_t* y, uint8_t* q,
+                      float* scale, void* stream);
+
+/*
+ * moe_rmsnorm_backward: its gradient from the stream h that the norm read
+ * (moe_rmsnorm_quant's h, or its x where there is no residual). With
+ * r = 1 / sqrt(mean(h^2) + eps), n = h r, g = dy w:
+ *   dh = dres + r (g - n mean(g n)),   dw = sum over the rows of dy n
+ * dh is the gradient of the stream and of x alike. The E4M3 output is a cast
+ * (its gradient passes through): dy is the whole gradient of y.
+ *   dy     [rows][d] bf16
+ *   h      [rows][d] bf16, or FP32 when stream_is_fp32
+ *   w      [d] FP32, or bf16 when w_is_bf16
+ *   dres   NULL (zero), or [rows][d] of h's type: what reaches the stream
+ *          past the norm
+ *   dh     [rows][d] of h's type (out); may alias dres or h
+ *   dw     [d] FP32 (out)
+ *   workspace  moe_rmsnorm_backward_workspace(rows, d) bytes, 16-byte aligned
+ * Sums are FP32 in an order that the sizes alone fix: no atomics. rows = 0
+ * gives dw = 0. Limits: d a multiple of 8, at most 16384.
+ */
+MOE_API size_t moe_rmsnorm_backward_workspace(int rows, int d);
+MOE_API int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int stream_is_fp32,
+                         const void* w, int w_is_bf16, float eps, const void* dres,
+                         int rows, int d, void* dh, float* dw, void* workspace,
+                         size_t ws_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------- few tokens
+ * moe_few_tokens: the whole layer for 1 <= T <= 16 tokens in one kernel (and
+ * one small memset before it), for single-stream and small-batch decoding:
+ * moe_route, moe_quant_1x128, the experts of moe_grouped_gemm_fp8 and
+ * moe_combine ("DeepSeek-V3 Teknik Raporu", Yöntem 2 and Temel fikirler, FP8
+ * bullet; the pages have no such kernel). Each touched expert's weights are
+ * read once.
+ *   u        [T][d] bf16: the router's input, and the experts' unless xq is given
+ *   xq, xs   both NULL (u is quantised inside, bit for bit as moe_quant_1x128
+ *            does), or the experts' input [T][d] E4M3, [T][d/128] FP32
+ *   base     NULL (u), or [T][d] bf16: what the experts' sum is added to (the
+ *            residual stream in front of a pre-norm)
+ *   e, b     [N_r][d] bf16 centroids, [N_r] FP32 routing bias
+ *   w_*, s_* as in moe_grouped_gemm_fp8 (N_r + 1 slots, slot N_r shared)
+ *   out      [T][d] bf16 (out): base + shared + sum_k gate_k expert_k, summed in
+ *            FP32 and rounded once (the layer's separate calls round every
+ *            expert's output to bf16 before the sum); may alias base or u
+ *   topk_idx, gates  [T][K_r] int32, FP32 (out), ordered as moe_route orders them
+ *   counts   NULL, or [N_r] int32 (out): tokens of each expert (moe_bias_update)
+ *   workspace  moe_few_tokens_workspace(...) bytes, 16-byte aligned; its first
+ *            bytes are zeroed by every call on its stream
+ * The logits are summed in FP64 and each affinity is rounded once to FP32, so
+ * the selection is that of the exact affinities in FP32 keys; a NaN key sorts
+ * below every other. The kernel is a cooperative launch of one CTA per SM: its
+ * CTAs wait for one another, so two calls that share a workspace must not
+ * overlap (calls with workspaces of their own may). Results do not depend on
+ * the schedule. T = 0 only zeroes counts.
+ * Limits: K_r <= 16, K_r <= N_r <= 256, d a multiple of 256 up to 8192, I a
+ * multiple of 128 up to 8192, and T rows of d, or 2 T rows of I, within shared
+ * memory beside three stages of weights (else MOE_ERR_UNSUPPORTED: at T = 16,
+ * I up to 4096; at T = 8, any).
+ * moe_few_tokens_workspace returns 0 for sizes outside the limits.
+ */
+MOE_API size_t moe_few_tokens_workspace(int T, int d, int N_r, int K_r, int I);
+MOE_API int moe_few_tokens(const uint16_t* u, const uint8_t* xq, const float* xs,
+                   const uint16_t* base, const uint16_t* e, const float* b,
+                   int T, int d, int N_r, int K_r, const uint8_t* w_gate,
+                   const uint8_t* w_up, const uint8_t* w_down,
+                   const float* s_gate, const float* s_up, const float* s_down,
+                   int I, uint16_t* out, int32_t* topk_idx, float* gates,
+                   int32_t* counts, void* workspace, size_t ws_bytes,
+                   void* stream);
+
+/*
  * moe_debug_wait_timeout: launches one block that waits on a barrier nothing
  * ever signals, with a limit of timeout_us microseconds; the wait gives up and
  * records MOE_ERR_TIMEOUT in the device error word. Exists to test the

@@ -132,6 +132,27 @@ def route(u, e, b, K: int):
 
 
 # --------------------------------------------------------------------------
+# Pre-norm: what makes u_t. Not on the pages (they start at u_t); the usual
+# root-mean-square norm with the residual's addition in front.
+# --------------------------------------------------------------------------
+
+def rmsnorm(s, w, eps: float) -> np.ndarray:
+    """y = s / sqrt(mean(s^2) + eps) * w over the last axis, float64."""
+    s = np.asarray(s, np.float64)
+    return s / np.sqrt((s ** 2).mean(axis=-1, keepdims=True) + eps) * np.asarray(w, np.float64)
+
+
+def rmsnorm_backward(dy, h, w, eps: float, dres=None):
+    """(dh, dw) of y = rmsnorm(h, w): with r = 1 / sqrt(mean(h^2) + eps),
+    n = h r, g = dy w: dh = dres + r (g - n mean(g n)), dw = sum_t dy n."""
+    dy, h, w = (np.asarray(x, np.float64) for x in (dy, h, w))
+    r = 1.0 / np.sqrt((h ** 2).mean(axis=-1, keepdims=True) + eps)
+    n, g = h * r, dy * w
+    dh = r * (g - n * (g * n).mean(axis=-1, keepdims=True))
+    return (dh if dres is None else dh + np.asarray(dres, np.float64)), (dy * n).sum(axis=0)
+
+
+# --------------------------------------------------------------------------
 # Permutation. The pages group tokens per expert without printing how; the
 # reading taken is a stable counting sort: rows ordered by (expert asc, token
 # asc). This function is that order's definition; the histogram / prefix-sum
