@@ -28,20 +28,30 @@ constexpr int MAX_ENTRIES = MAX_T * MAX_K + MAX_T;
 constexpr int CW = 8;                        // multiplying warps
 constexpr int KC = CW * 128;                 // channels of a stage: one 128-block a warp
 constexpr int ROWS = 16;                     // weight rows of a stage
-constexpr int PITCH = KC + 64;               // rows of 16-byte words on distinct banks
-constexpr int STAGE = ROWS * PITCH;
+constexpr int STAGE = ROWS * KC;
 constexpr int MAX_STAGES = 12;
 constexpr int MAX_HBUF = 4;
 constexpr int MAX_TILES = 4;                 // 16-row tiles of W_down a CTA owns
 constexpr int RCOL = 20;                     // padded rows of a reduction column
-constexpr int THREADS = (CW + 1 + 4) * 32;
+constexpr int THREADS = (CW + 1 + 3) * 32;   // 12 warps: 168 registers a thread
 constexpr int SMEM_MAX = 227 * 1024;
 
 // NT: 8-token tiles. EW: warps that finish units of the first phase.
 template <int NT> struct Shape {
-  static constexpr int EW = NT == 1 ? 4 : 2;
+  static constexpr int EW = NT == 1 ? 3 : 2;
   static constexpr int RED = CW * NT * 8 * RCOL;      // floats of one unit's partials
 };
+
+// Tensor maps of the weights, rows [slot * rows] by 128-byte blocks: a box is
+// R rows by KC / 128 blocks, stored [block][row][128] with the 128-byte swizzle.
+struct Maps {
+  CUtensorMap gate, up;     // R = 8
+  CUtensorMap down[5];      // R = 1 << i
+};
+
+// Bytes of a row of n bytes such that neighbouring rows start 16 bytes apart
+// modulo 128 (n a multiple of 16).
+__host__ __device__ constexpr int pitch_of(int n) { return ((n + 111) & ~127) + 16; }
 
 struct Args {
   const uint16_t* u;
@@ -52,7 +62,6 @@ struct Args {
   const float* xs;
   uint8_t* xq_ws;           // not NULL: quantise u into the workspace
   float* xs_ws;
-  const uint8_t *w_gate, *w_up, *w_down;
   const float *s_gate, *s_up, *s_down;
   uint16_t* out;
   int32_t* topk_idx;
@@ -92,6 +101,14 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
+__device__ __forceinline__ void box_load(void* dst, const CUtensorMap* m, uint64_t* bar, int row, int block) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(m), "r"(smem_u32(bar)), "r"(0), "r"(row), "r"(block)
+      : "memory");
+}
+
 __device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -128,17 +145,24 @@ __device__ __forceinline__ int range_begin(int i, int n, int parts) {
   return static_cast<int>(static_cast<long long>(i) * n / parts);
 }
 
-// Partial products of one 128-channel block of a stage: 16 weight rows of the
-// lane's warp (a) by the lane's column (x: 128 codes of its token, or NULL for
-// a column without a token). Word i of every 16-byte run is the same channel
-// on both sides, so the order of channels inside the block is free.
+// Partial products of one 128-channel block of a stage: 16 weight rows by
+// eight tokens. Lane q of a row's four holds channels 32 q .. 32 q + 31 on both
+// sides (the order of channels inside the block is free): two 16-byte words,
+// of which a swizzled weight row and an activation row with a pitch of 16
+// modulo 128 bytes each serve eight lanes on distinct banks.
 struct Frag {
   uint32_t w[8];
 };
-__device__ __forceinline__ Frag load_frag(const uint8_t* p) {
-  const uint4 lo = *reinterpret_cast<const uint4*>(p);
-  const uint4 hi = *reinterpret_cast<const uint4*>(p + 64);
+__device__ __forceinline__ Frag frag_of(const uint4 lo, const uint4 hi) {
   return Frag{{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
+}
+__device__ __forceinline__ Frag weight_frag(const uint8_t* row, int q4) {    // row: 128 bytes of a swizzled box
+  const int x = (smem_u32(row) >> 7) & 7;
+  return frag_of(*reinterpret_cast<const uint4*>(row + (((2 * q4) ^ x) << 4)),
+                 *reinterpret_cast<const uint4*>(row + (((2 * q4 + 1) ^ x) << 4)));
+}
+__device__ __forceinline__ Frag token_frag(const uint8_t* p) {
+  return frag_of(*reinterpret_cast<const uint4*>(p), *reinterpret_cast<const uint4*>(p + 16));
 }
 __device__ __forceinline__ void block_product(float (&c)[4], const Frag& r0, const Frag& r8, const Frag& x) {
 #pragma unroll
@@ -146,6 +170,23 @@ __device__ __forceinline__ void block_product(float (&c)[4], const Frag& r0, con
     const uint32_t a[4] = {r0.w[2 * j], r8.w[2 * j], r0.w[2 * j + 1], r8.w[2 * j + 1]};
     mma_e4m3(c, a, x.w[2 * j], x.w[2 * j + 1]);
   }
+}
+
+// Row r of a tile of n rows: the rows of the box that holds it (the bits of n,
+// largest first), and its offset in the stage.
+__device__ __forceinline__ int box_rows(int r, int n) {
+  int at = 0;
+#pragma unroll
+  for (int b = 4; b >= 0; --b) {
+    if (!((n >> b) & 1)) continue;
+    if (r < at + (1 << b)) return 1 << b;
+    at += 1 << b;
+  }
+  return 1;
+}
+__device__ __forceinline__ int box_offset(int r, int n) {
+  const int R = box_rows(r, n), at = n & ~(2 * R - 1);
+  return at * KC + (r - at) * 128;
 }
 
 // ---------------------------------------------------------------- router
@@ -383,10 +424,10 @@ __device__ __forceinline__ void unit_at(const Args& a, const Units& u, int i, in
 // ---------------------------------------------------------------- kernel
 
 template <int NT>
-__global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const Args a) {
+__global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_constant__ Maps maps, const Args a) {
   constexpr int EW = Shape<NT>::EW;
   constexpr int RED = Shape<NT>::RED;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem;
   uint8_t* xh = smem + static_cast<size_t>(a.stages) * STAGE;        // tokens' codes, then the H rows
   float* red = reinterpret_cast<float*>(xh + a.xh_bytes);            // [EW][CW][8 NT][RCOL]
@@ -394,8 +435,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const Args a) {
   Small* sm = reinterpret_cast<Small*>(xs + ((a.T * (a.d >> 7) + 3) & ~3));
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int xpitch = a.d + 64;
-  const int hpitch = ((a.hrec_bytes + 63) & ~127) + 64;
+  const int xpitch = pitch_of(a.d), hpitch = pitch_of(a.hrec_bytes);
   volatile int* abort = &sm->abort;
 
   for (int i = threadIdx.x; i < MAX_SLOTS; i += THREADS) sm->mask[i] = 0u;
@@ -411,7 +451,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const Args a) {
 
   const int row0 = range_begin(blockIdx.x, a.d, gridDim.x);           // rows of W_down
   const int nrows = range_begin(blockIdx.x + 1, a.d, gridDim.x) - row0;
-  const int ntiles = (nrows + ROWS - 1) / ROWS;
+  const int ntiles = (nrows + ROWS - 1) / ROWS;                       // the last one may be short
   Units un;
   shared_units(a, un);
 
@@ -419,24 +459,24 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const Args a) {
     // ------------------------------------------------------------ producer
     int it = 0;
     bool ok = true;
-    auto stage_rows = [&](const uint8_t* src, size_t ld, int n, int k, int kc) {   // lane's row of n at k
+    auto claim = [&](uint32_t bytes) -> uint8_t* {       // the next stage, expecting so many bytes
       const int s = it % a.stages;
       if (ok && it >= a.stages) ok = warp_wait(&sm->empty[s], ((it / a.stages) - 1) & 1, abort);
       if (ok) {
-        if (lane == 0) mbar_arrive_expect_tx(&sm->full[s], n * kc);
-        __syncwarp();
-        if (lane < n) bulk_load(ring + s * STAGE + lane * PITCH, src + static_cast<size_t>(lane) * ld + k, kc, &sm->full[s]);
         ++it;
+        if (lane == 0) mbar_arrive_expect_tx(&sm->full[s], bytes);
+        __syncwarp();
       }
+      return ring + s * STAGE;
     };
     auto gate_up = [&](int i) {
       int slot, row;
       unit_at(a, un, i, slot, row);
-      const int ex = slot == 0 ? a.N_r : sm->slot_expert[slot];
-      const size_t at = (static_cast<size_t>(ex) * a.I + row) * a.d;
-      // lanes 0..7 the gate rows, 8..15 the up rows
-      const uint8_t* src = (lane < 8 ? a.w_gate + at : a.w_up + at) - (lane < 8 ? 0 : static_cast<size_t>(8) * a.d);
-      for (int k = 0; k < a.d; k += KC) stage_rows(src, a.d, ROWS, k, min(KC, a.d - k));
+      row += (slot == 0 ? a.N_r : sm->slot_expert[slot]) * a.I;
+      for (int k = 0; k < a.d; k += KC) {
+        uint8_t* dst = claim(STAGE);
+        if (ok && lane < 2) box_load(dst + lane * (STAGE / 2), lane == 0 ? &maps.gate : &maps.up, &sm->full[(it - 1) % a.stages], row, k >> 7);
+      }
     };
     for (int i = 0; i < un.sh1 - un.sh0; ++i) gate_up(i);
     ok = warp_wait(&sm->sel_ready, 0, abort) && ok;
@@ -445,11 +485,16 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const Args a) {
       routed_units(a, slots, un);
       for (int i = un.sh1 - un.sh0; i < un.count(); ++i) gate_up(i);
       for (int si = 0; si < slots; ++si) {
-        const uint8_t* w = a.w_down + (static_cast<size_t>(sm->slot_expert[si]) * a.d + row0) * a.I;
+        const int row = sm->slot_expert[si] * a.d + row0;
         for (int t = 0; t < ntiles; ++t) {
-          const int r = range_begin(t, nrows, ntiles), n = range_begin(t + 1, nrows, ntiles) - r;
-          for (int k = 0; k < a.I; k += KC)
-            stage_rows(w + static_cast<size_t>(r) * a.I, a.I, n, k, min(KC, a.I - k));
+          // a short tile is the boxes of its row count's bits, largest first
+          const int n = min(ROWS, nrows - t * ROWS);
+          const int bit = 4 - lane, above = lane > 0 && lane < 5 ? n & ~((2 << bit) - 1) : 0;
+          for (int k = 0; k < a.I; k += KC) {
+            uint8_t* dst = claim(n * KC);
+            if (ok && lane < 5 && ((n >> bit) & 1))
+              box_load(dst + above * KC, &maps.down[bit], &sm->full[(it - 1) % a.stages], row + t * ROWS + above, k >> 7);
+          }
         }
       }
     }
@@ -594,12 +639,12 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const Args a) {
         const float fg = mine ? __ldg(sg + kb) : 0.0f, fu = mine ? __ldg(su + kb) : 0.0f;
         ok = ok && warp_wait(&sm->full[s], (it / a.stages) & 1, abort);
         if (ok && mine) {
-          const uint8_t* p = ring + s * STAGE + g * PITCH + warp * 128 + q4 * 16;
-          const Frag r0 = load_frag(p), r8 = load_frag(p + 8 * PITCH);
+          const uint8_t* p = ring + s * STAGE + warp * 1024 + g * 128;
+          const Frag r0 = weight_frag(p, q4), r8 = weight_frag(p + STAGE / 2, q4);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             if (n * 8 < ntok) {
-              const Frag x = load_frag(xh + tok[n] * xpitch + kb * 128 + q4 * 16);
+              const Frag x = token_frag(xh + tok[n] * xpitch + kb * 128 + q4 * 32);
               float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
               block_product(c, r0, r8, x);
               const float x0 = xs[c0[n] + kb], x1 = xs[c1[n] + kb];
@@ -661,8 +706,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const Args a) {
 #pragma unroll
       for (int t = 0; t < MAX_TILES; ++t) {
         if (t >= ntiles) continue;
-        const int r = range_begin(t, nrows, ntiles), nr = range_begin(t + 1, nrows, ntiles) - r;
-        const int n0 = (row0 + r + min(g, nr - 1)) >> 7, n8 = (row0 + r + min(g + 8, nr - 1)) >> 7;
+        const int nr = min(ROWS, nrows - t * ROWS);
+        const int ra = min(g, nr - 1), rb = min(g + 8, nr - 1);          // rows past a short tile repeat its last
+        const int oa = box_offset(ra, nr) + warp * box_rows(ra, nr) * 128, ob = box_offset(rb, nr) + warp * box_rows(rb, nr) * 128;
+        const int n0 = (row0 + t * ROWS + ra) >> 7, n8 = (row0 + t * ROWS + rb) >> 7;
         const float* s0 = a.s_down + (static_cast<size_t>(ex) * kb_d + n0) * kb_i;
         const float* s8 = a.s_down + (static_cast<size_t>(ex) * kb_d + n8) * kb_i;
         for (int k0 = 0; k0 < a.I; k0 += KC, ++it) {
@@ -672,13 +719,13 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const Args a) {
           const float f0 = mine ? __ldg(s0 + kb) : 0.0f, f8 = mine ? __ldg(s8 + kb) : 0.0f;
           ok = ok && warp_wait(&sm->full[s], (it / a.stages) & 1, abort);
           if (ok && mine) {
-            const uint8_t* p = ring + s * STAGE + g * PITCH + warp * 128 + q4 * 16;
-            const Frag r0 = load_frag(p), r8 = load_frag(p + 8 * PITCH);
+            const uint8_t* p = ring + s * STAGE;
+            const Frag r0 = weight_frag(p + oa, q4), r8 = weight_frag(p + ob, q4);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               if ((mask >> (n * 8)) & 0xFFu) {
                 Frag x = {{0, 0, 0, 0, 0, 0, 0, 0}};
-                if (col[n] != nullptr) x = load_frag(col[n] + kb * 128 + q4 * 16);
+                if (col[n] != nullptr) x = token_frag(col[n] + kb * 128 + q4 * 32);
                 __syncwarp();
                 float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 block_product(c, r0, r8, x);
@@ -718,14 +765,12 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const Args a) {
     named_bar_sync(1, CW * 32);
     const uint16_t* base = a.base != nullptr ? a.base : a.u;
     for (int o = tid; o < a.T * 64; o += CW * 32) {
-      const int t = o >> 6, tile = (o >> 4) & 3, r = o & 15;
-      if (tile >= ntiles) continue;
-      const int b0 = range_begin(tile, nrows, ntiles);
-      if (r >= range_begin(tile + 1, nrows, ntiles) - b0) continue;
+      const int t = o >> 6, r = o & 63;
+      if (r >= nrows) continue;
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < CW; ++w) v += fin[(w * 8 * NT + t) * 64 + (o & 63)];
-      const size_t at = static_cast<size_t>(t) * a.d + row0 + b0 + r;
+      for (int w = 0; w < CW; ++w) v += fin[(w * 8 * NT + t) * 64 + r];
+      const size_t at = static_cast<size_t>(t) * a.d + row0 + r;
       a.out[at] = float_to_bf16_bits(bf16_bits_to_float(base[at]) + v);
     }
   }
@@ -760,9 +805,22 @@ inline bool sizes_supported(int T, int d, int N_r, int K_r, int I) {
          I % 128 == 0 && I <= 8192;
 }
 
+// [rows][cols] codes as (128, rows, cols / 128), boxes of R rows by KC / 128 blocks.
+inline int make_map(CUtensorMap* m, const void* base, size_t rows, int cols, int R) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return record_failure(MOE_ERR_CUDA, "cuTensorMapEncodeTiled", "entry point not found");
+  cuuint64_t dims[3] = {128, rows, static_cast<cuuint64_t>(cols / 128)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols), 128};
+  cuuint32_t box[3] = {128, static_cast<cuuint32_t>(R), KC / 128}, one[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, one,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MOE_OK : record_failure(MOE_ERR_CUDA, "cuTensorMapEncodeTiled", "few tokens: weight map");
+}
+
 template <int NT>
-int launch(Args& a, const DeviceInfo& di, cudaStream_t s) {
-  const int xpitch = a.d + 64, hpitch = ((a.hrec_bytes + 63) & ~127) + 64;
+int launch(const Maps& maps, Args& a, const DeviceInfo& di, cudaStream_t s) {
+  const int xpitch = pitch_of(a.d), hpitch = pitch_of(a.hrec_bytes);
   const int one = a.T * hpitch;
   int xh = a.T * xpitch > 2 * one ? a.T * xpitch : 2 * one;
   a.hbufs = xh / one;
@@ -788,7 +846,7 @@ int launch(Args& a, const DeviceInfo& di, cudaStream_t s) {
   at[0].val.cooperative = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, k, static_cast<const Args>(a)), "few tokens: launch");
+  return cuda_status(cudaLaunchKernelEx(&cfg, k, maps, static_cast<const Args>(a)), "few tokens: launch");
 }
 
 }  // namespace few
@@ -831,7 +889,6 @@ extern "C" int moe_few_tokens(const uint16_t* u, const uint8_t* xq, const float*
   a.xs_ws = xq ? nullptr : reinterpret_cast<float*>(ws + l.xs);
   a.xq = xq ? xq : a.xq_ws;
   a.xs = xq ? xs : a.xs_ws;
-  a.w_gate = w_gate; a.w_up = w_up; a.w_down = w_down;
   a.s_gate = s_gate; a.s_up = s_up; a.s_down = s_down;
   a.out = out; a.topk_idx = topk_idx; a.gates = gates; a.counts = counts;
   a.grid_ctr = reinterpret_cast<unsigned*>(ws);
@@ -841,6 +898,12 @@ extern "C" int moe_few_tokens(const uint16_t* u, const uint8_t* xq, const float*
   a.hrec = ws + l.hrec;
   a.hrec_bytes = l.hrec_bytes;
   a.T = T; a.d = d; a.N_r = N_r; a.K = K_r; a.I = I;
+  Maps maps;
+  const size_t G = static_cast<size_t>(N_r) + 1;
+  if (int st = make_map(&maps.gate, w_gate, G * I, d, 8)) return st;
+  if (int st = make_map(&maps.up, w_up, G * I, d, 8)) return st;
+  for (int i = 0; i < 5; ++i)
+    if (int st = make_map(&maps.down[i], w_down, G * d, I, 1 << i)) return st;
   if (int st = cuda_status(cudaMemsetAsync(ws, 0, l.ctr_bytes, s), "few tokens: counters")) return st;
-  return T <= 8 ? launch<1>(a, di, s) : launch<2>(a, di, s);
+  return T <= 8 ? launch<1>(maps, a, di, s) : launch<2>(maps, a, di, s);
 }
