@@ -3,18 +3,19 @@
 //
 // Every byte of the touched experts' weights is read once and nothing else is
 // large, so the kernel is a stream of weights: one CTA per SM (a cooperative
-// launch), a producer warp that keeps a ring of bulk copies in flight across
-// all phases, and eight warps that multiply. The weights do not depend on the
-// exchange between the phases, only on the selection, so the ring fills with
-// the shared expert while the router runs and with W_down while the last
-// intermediate rows are written.
+// launch), a producer that keeps a ring of TMA boxes in flight across all
+// phases, and the tensor cores behind it. The weights do not depend on what the
+// phases exchange, only on the selection, so the ring fills with the shared
+// expert while the router runs and with W_down while the last intermediate rows
+// are written.
 //
-// The products run on the register tensor-core path (m16n8k32, E4M3): 16
-// weight rows by 8 tokens. Tokens fill at most two such tiles, the products
-// need a small part of its rate, and its 16-row granularity splits the rows of
-// W_gate, W_up and W_down evenly over the SMs, which 128-row TMEM tiles cannot
-// (one token: 9 experts are 144 tiles in the first phase and 252 in the
-// second, for 148 SMs).
+// Products: weight rows are the MMA's M side (128, of which 64 are live: a unit
+// of the first phase is 32 gate and the matching 32 up rows, the second phase
+// has the CTA's own d / SMs rows of W_down), tokens its N side (16, those
+// behind T ignored). The 64 live rows are a choice of balance: one token has 9
+// experts, 576 such units for 148 SMs (0.97 of them busy in the last round),
+// and MMAs with half of their rows dead still take under half of the time that
+// their 8 KB of weights take to arrive.
 #include "host.cuh"
 
 namespace moe {
@@ -25,33 +26,30 @@ constexpr int MAX_K = 16;
 constexpr int MAX_N = 256;
 constexpr int MAX_SLOTS = MAX_N + 1;
 constexpr int MAX_ENTRIES = MAX_T * MAX_K + MAX_T;
-constexpr int CW = 8;                        // multiplying warps
-constexpr int KC = CW * 128;                 // channels of a stage: one 128-block a warp
-constexpr int ROWS = 16;                     // weight rows of a stage
-constexpr int STAGE = ROWS * KC;
+constexpr int MAX_D = 8192;
+constexpr int CW = 8;                        // warps of the router and the selection
+constexpr int EW = 3;                        // of them, finishing warps of the first phase
+constexpr int THREADS = (CW + 2) * 32;       // and the producer, the MMA issuer
+constexpr int CH = 32;                       // intermediate channels of a unit
+constexpr int LIVE = 64;                     // live weight rows of a tile
+constexpr int SK = 2;                        // 128-channel blocks of a stage
+constexpr int TILE = LIVE * 128;             // bytes of one block of a stage
+constexpr int STAGE = SK * TILE;
 constexpr int MAX_STAGES = 12;
 constexpr int MAX_HBUF = 4;
-constexpr int MAX_TILES = 4;                 // 16-row tiles of W_down a CTA owns
-constexpr int RCOL = 20;                     // padded rows of a reduction column
-constexpr int THREADS = (CW + 1 + 3) * 32;   // 12 warps: 168 registers a thread
+constexpr int COLS = 16;                     // MMA columns: tokens
+constexpr int QS = 2;                        // sums of a block's four K = 32 steps: even and odd ones apart
+constexpr int BUF_COLS = SK * QS * COLS;     // TMEM columns of a stage's partials
+constexpr int BUFS = 8;
+constexpr int TMEM_COLS = BUFS * BUF_COLS;
+constexpr int RED = 2 * COLS * CH;           // floats of one unit's sums
 constexpr int SMEM_MAX = 227 * 1024;
 
-// NT: 8-token tiles. EW: warps that finish units of the first phase.
-template <int NT> struct Shape {
-  static constexpr int EW = NT == 1 ? 3 : 2;
-  static constexpr int RED = CW * NT * 8 * RCOL;      // floats of one unit's partials
-};
-
-// Tensor maps of the weights, rows [slot * rows] by 128-byte blocks: a box is
-// R rows by KC / 128 blocks, stored [block][row][128] with the 128-byte swizzle.
+// Maps of the weights, rows [slot * rows] of codes, boxes of 128 channels by:
 struct Maps {
-  CUtensorMap gate, up;     // R = 8
-  CUtensorMap down[5];      // R = 1 << i
+  CUtensorMap gate, up;                      // CH rows, SK blocks: stored [block][row][128]
+  CUtensorMap down[2];                       // a CTA's rows of W_down, by the parity of their count
 };
-
-// Bytes of a row of n bytes such that neighbouring rows start 16 bytes apart
-// modulo 128 (n a multiple of 16).
-__host__ __device__ constexpr int pitch_of(int n) { return ((n + 111) & ~127) + 16; }
 
 struct Args {
   const uint16_t* u;
@@ -67,31 +65,49 @@ struct Args {
   int32_t* topk_idx;
   float* gates;
   int32_t* counts;
-  unsigned* grid_ctr;       // two grid barriers, 128 bytes apart
-  int* blk_ctr;             // [slot][I/128]: finished 8-row units of a block
-  float* scores;            // [T][N_r]
+  unsigned* grid_ctr;       // CTAs whose affinities are written
+  unsigned* slot_done;      // [slot] quantised blocks of its H
+  int* blk_ctr;             // [slot][I/128]: finished units of a block
+  float2* scores;           // [T][N_r] key s + b, affinity s
   float* act;               // [T*K + T][I] silu(G) U
-  uint8_t* hrec;            // [T*K + T][hrec_bytes]: I codes, then I/128 scales
+  uint8_t* hq;              // [T*K + T][I] its codes, 16-byte words swizzled by token
+  float* hs;                // [T*K + T][I/128]
   int T, d, N_r, K, I;
-  int stages, hbufs, xh_bytes, hrec_bytes;
+  int rows8;                // token rows of an operand tile: 8 or 16
+  int stages, hbufs, xh_bytes, hbuf_bytes;
 };
 
 // Shared memory behind the dynamic regions.
 struct Small {
   uint64_t full[MAX_STAGES], empty[MAX_STAGES];
   uint64_t hfull[MAX_HBUF], hempty[MAX_HBUF];
-  uint64_t redfull[4], redempty[4];
-  uint64_t sel_ready;
+  uint64_t tfull[BUFS], tempty[BUFS];
+  uint64_t redfull[EW], redempty[EW];
+  uint64_t sel_ready, x_free, drained;
+  uint32_t tmem;
   int abort;
   int n_slots;
-  uint32_t mask[MAX_SLOTS];                  // tokens of expert i
+  uint32_t mask[MAX_N];                      // tokens of expert i
   uint16_t slot_expert[MAX_SLOTS];
-  uint16_t slot_of[MAX_SLOTS];
+  uint16_t slot_of[MAX_N];
   uint16_t slot_start[MAX_SLOTS + 1];
-  uint16_t ent_row[MAX_ENTRIES];             // row of act and hrec
+  uint16_t ent_row[MAX_ENTRIES];             // row of act, hq and hs
   uint8_t ent_tok[MAX_ENTRIES];
   float ent_gate[MAX_ENTRIES];
-  double dots[CW][16];
+  int chunk_slots[CW], chunk_ents[CW];
+  double dots[CW][32];
+};
+
+// A position in a ring of barriers: index and the parity of its lap.
+struct Cursor {
+  int i = 0;
+  uint32_t lap = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++i == n) {
+      i = 0;
+      lap ^= 1;
+    }
+  }
 };
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -101,6 +117,7 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
+// One box of [rows][blocks of 128]: coordinates row and block.
 __device__ __forceinline__ void box_load(void* dst, const CUtensorMap* m, uint64_t* bar, int row, int block) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
@@ -109,20 +126,15 @@ __device__ __forceinline__ void box_load(void* dst, const CUtensorMap* m, uint64
       : "memory");
 }
 
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
-__device__ __forceinline__ void grid_arrive(unsigned* ctr) {
+__device__ __forceinline__ void count_up(unsigned* ctr) {
   __threadfence();
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(ctr) : "memory");
 }
 
-// Waits until all CTAs have arrived; bounded as mbar_wait is.
-__device__ __forceinline__ bool grid_wait(const unsigned* ctr, unsigned n, volatile int* abort) {
+// Waits until a counter has reached n; bounded as mbar_wait is.
+__device__ __forceinline__ bool count_wait(const unsigned* ctr, unsigned n, volatile int* abort) {
   uint64_t t0 = 0;
   for (uint32_t i = 0;; ++i) {
     unsigned v;
@@ -141,61 +153,17 @@ __device__ __forceinline__ bool grid_wait(const unsigned* ctr, unsigned n, volat
   }
 }
 
-__device__ __forceinline__ int range_begin(int i, int n, int parts) {
+__host__ __device__ inline int range_begin(int i, int n, int parts) {
   return static_cast<int>(static_cast<long long>(i) * n / parts);
-}
-
-// Partial products of one 128-channel block of a stage: 16 weight rows by
-// eight tokens. Lane q of a row's four holds channels 32 q .. 32 q + 31 on both
-// sides (the order of channels inside the block is free): two 16-byte words,
-// of which a swizzled weight row and an activation row with a pitch of 16
-// modulo 128 bytes each serve eight lanes on distinct banks.
-struct Frag {
-  uint32_t w[8];
-};
-__device__ __forceinline__ Frag frag_of(const uint4 lo, const uint4 hi) {
-  return Frag{{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
-}
-__device__ __forceinline__ Frag weight_frag(const uint8_t* row, int q4) {    // row: 128 bytes of a swizzled box
-  const int x = (smem_u32(row) >> 7) & 7;
-  return frag_of(*reinterpret_cast<const uint4*>(row + (((2 * q4) ^ x) << 4)),
-                 *reinterpret_cast<const uint4*>(row + (((2 * q4 + 1) ^ x) << 4)));
-}
-__device__ __forceinline__ Frag token_frag(const uint8_t* p) {
-  return frag_of(*reinterpret_cast<const uint4*>(p), *reinterpret_cast<const uint4*>(p + 16));
-}
-__device__ __forceinline__ void block_product(float (&c)[4], const Frag& r0, const Frag& r8, const Frag& x) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t a[4] = {r0.w[2 * j], r8.w[2 * j], r0.w[2 * j + 1], r8.w[2 * j + 1]};
-    mma_e4m3(c, a, x.w[2 * j], x.w[2 * j + 1]);
-  }
-}
-
-// Row r of a tile of n rows: the rows of the box that holds it (the bits of n,
-// largest first), and its offset in the stage.
-__device__ __forceinline__ int box_rows(int r, int n) {
-  int at = 0;
-#pragma unroll
-  for (int b = 4; b >= 0; --b) {
-    if (!((n >> b) & 1)) continue;
-    if (r < at + (1 << b)) return 1 << b;
-    at += 1 << b;
-  }
-  return 1;
-}
-__device__ __forceinline__ int box_offset(int r, int n) {
-  const int R = box_rows(r, n), at = n & ~(2 * R - 1);
-  return at * KC + (r - at) * 128;
 }
 
 // ---------------------------------------------------------------- router
 
-// Affinities of experts e0 and e1 (e1 < 0: none) with eight tokens from t0.
-// The selection is a border, so the logits are summed in FP64 (their products
-// are exact) and the affinity is rounded once: keys that differ in FP32 are
-// never exchanged by the sum's order. Costs 16 conversions and DFMAs a clock
-// and SM while the ring fills.
+// Affinities of experts e0 and e1 (e1 < 0: none) with every token. The
+// selection is a border, so the logits are summed in FP64 (their products are
+// exact) and the affinity is rounded once: keys that differ in FP32 are never
+// exchanged by the sum's order. FP64 costs conversions and DFMAs, which run
+// while the ring fills.
 __device__ __forceinline__ void to_double8(const uint4 v, double (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -205,50 +173,64 @@ __device__ __forceinline__ void to_double8(const uint4 v, double (&f)[8]) {
   }
 }
 
-__device__ __forceinline__ void affinities(const Args& a, Small* sm, int e0, int e1, int t0) {
+__device__ __forceinline__ void affinities(const Args& a, Small* sm, int e0, int e1) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  double acc[16];
+  double acc[32];                            // [expert][token]
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.0;
+  for (int i = 0; i < 32; ++i) acc[i] = 0.0;
   const int V = a.d >> 3;
-  for (int v = tid; v < V; v += CW * 32) {
+  const uint4* r0 = reinterpret_cast<const uint4*>(a.e + static_cast<size_t>(e0) * a.d);
+  const uint4* r1 = reinterpret_cast<const uint4*>(a.e + static_cast<size_t>(e1 < 0 ? e0 : e1) * a.d);
+  const uint4* ru = reinterpret_cast<const uint4*>(a.u);
+  int v = tid;
+  uint4 n0 = make_uint4(0, 0, 0, 0), n1 = n0;
+  if (v < V) { n0 = __ldg(r0 + v); n1 = __ldg(r1 + v); }
+  for (; v < V; v += CW * 32) {
     double w0[8], w1[8];
-    to_double8(__ldg(reinterpret_cast<const uint4*>(a.e + static_cast<size_t>(e0) * a.d) + v), w0);
-    to_double8(__ldg(reinterpret_cast<const uint4*>(a.e + static_cast<size_t>(e1 < 0 ? e0 : e1) * a.d) + v), w1);
+    to_double8(n0, w0);
+    to_double8(n1, w1);
+    if (v + CW * 32 < V) { n0 = __ldg(r0 + v + CW * 32); n1 = __ldg(r1 + v + CW * 32); }
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      if (t0 + t < a.T) {
-        double x[8];
-        to_double8(__ldg(reinterpret_cast<const uint4*>(a.u + static_cast<size_t>(t0 + t) * a.d) + v), x);
+    for (int t0 = 0; t0 < MAX_T; t0 += 8) {
+      uint4 x[8];                            // eight tokens' runs at once: one latency
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          acc[t] = fma(x[j], w0[j], acc[t]);
-          acc[8 + t] = fma(x[j], w1[j], acc[8 + t]);
+      for (int t = 0; t < 8; ++t)
+        if (t0 + t < a.T) x[t] = __ldg(ru + static_cast<size_t>(t0 + t) * V + v);
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+        if (t0 + t < a.T) {
+          double f[8];
+          to_double8(x[t], f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            acc[t0 + t] = fma(f[j], w0[j], acc[t0 + t]);
+            acc[MAX_T + t0 + t] = fma(f[j], w1[j], acc[MAX_T + t0 + t]);
+          }
         }
-      }
     }
   }
-  // 16 sums over 32 lanes: each step halves the values a lane still holds
+  // 32 sums over 32 lanes: each step halves the values a lane still holds, and lane i ends with sum i
 #pragma unroll
-  for (int n = 8, o = 16; n >= 1; n >>= 1, o >>= 1) {
-    const bool up = lane & o;
+  for (int n = 16; n >= 1; n >>= 1) {
+    const bool up = lane & n;
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       const double give = up ? acc[i] : acc[i + n];
       const double keep = up ? acc[i + n] : acc[i];
-      acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, n);
     }
   }
-  acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 1);
-  // lane bits 4..1 chose the halves: value index = bits 16, 8, 4, 2 of the lane
-  if (!(lane & 1)) sm->dots[warp][lane >> 1] = acc[0];
+  sm->dots[warp][lane] = acc[0];
   named_bar_sync(1, CW * 32);
-  if (tid < 16) {
+  if (tid < 32) {
     double z = 0.0;
 #pragma unroll
     for (int w = 0; w < CW; ++w) z += sm->dots[w][tid];
-    const int t = t0 + (tid & 7), ex = tid < 8 ? e0 : e1;
-    if (t < a.T && ex >= 0) a.scores[t * a.N_r + ex] = static_cast<float>(1.0 / (1.0 + exp(-z)));
+    const int t = tid & (MAX_T - 1), ex = tid < MAX_T ? e0 : e1;
+    if (t < a.T && ex >= 0) {
+      const float s = static_cast<float>(1.0 / (1.0 + exp(-z)));
+      a.scores[t * a.N_r + ex] = make_float2(s + __ldg(a.b + ex), s);
+    }
   }
   named_bar_sync(1, CW * 32);
 }
@@ -301,8 +283,9 @@ __device__ __forceinline__ void select_token(const Args& a, int t, int& ex, floa
 #pragma unroll
   for (int j = 0; j < MAX_N / 32; ++j) {
     const int i = j * 32 + lane;
-    sc[j] = i < a.N_r ? __ldcg(a.scores + t * a.N_r + i) : 0.0f;
-    key[j] = i < a.N_r ? ordered(sc[j] + __ldg(a.b + i)) : 0u;      // 0: taken or absent
+    const float2 v = i < a.N_r ? __ldcg(a.scores + t * a.N_r + i) : make_float2(0.0f, 0.0f);
+    sc[j] = v.y;
+    key[j] = i < a.N_r ? ordered(v.x) : 0u;                          // 0: taken or absent
   }
   ex = 0;
   s = 0.0f;
@@ -346,32 +329,34 @@ __device__ __forceinline__ void select_all(const Args& a, Small* sm) {
     }
   }
   named_bar_sync(1, CW * 32);
-  if (warp == 0) {
-    int slots = 1, ents = a.T;
-    if (lane == 0) { sm->slot_expert[0] = a.N_r; sm->slot_start[0] = 0; }
-    for (int i0 = 0; i0 < a.N_r; i0 += 32) {
-      const int i = i0 + lane;
-      const uint32_t m = i < a.N_r ? sm->mask[i] : 0u;
-      const int n = __popc(m);
-      const uint32_t on = __ballot_sync(0xffffffffu, n > 0);
-      int pre = n;
+  {                                          // a warp lists 32 experts; the chunks' totals join them
+    const int i = warp * 32 + lane;
+    const int n = i < a.N_r ? __popc(sm->mask[i]) : 0;
+    const uint32_t on = __ballot_sync(0xffffffffu, n > 0);
+    int pre = n;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, pre, o);
-        if (lane >= o) pre += v;
-      }
-      if (n > 0) {
-        const int s = slots + __popc(on & ((1u << lane) - 1u));
-        sm->slot_expert[s] = i;
-        sm->slot_of[i] = s;
-        sm->slot_start[s] = ents + pre - n;
-      }
-      slots += __popc(on);
-      ents += __shfl_sync(0xffffffffu, pre, 31);
-      if (blockIdx.x == 0 && a.counts != nullptr && i < a.N_r) a.counts[i] = n;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += v;
     }
-    if (lane == 0) { sm->slot_start[slots] = ents; sm->n_slots = slots; }
-    if (lane < a.T) {
+    if (lane == 31) { sm->chunk_slots[warp] = __popc(on); sm->chunk_ents[warp] = pre; }
+    named_bar_sync(1, CW * 32);
+    int slots = 1, ents = a.T;
+    for (int w = 0; w < warp; ++w) { slots += sm->chunk_slots[w]; ents += sm->chunk_ents[w]; }
+    if (n > 0) {
+      const int s = slots + __popc(on & ((1u << lane) - 1u));
+      sm->slot_expert[s] = i;
+      sm->slot_of[i] = s;
+      sm->slot_start[s] = ents + pre - n;
+    }
+    if (blockIdx.x == 0 && a.counts != nullptr && i < a.N_r) a.counts[i] = n;
+    if (warp == CW - 1 && lane == 31) {
+      sm->slot_start[slots + __popc(on)] = ents + pre;
+      sm->n_slots = slots + __popc(on);
+      sm->slot_expert[0] = a.N_r;
+      sm->slot_start[0] = 0;
+    }
+    if (warp == 0 && lane < a.T) {
       sm->ent_tok[lane] = lane;
       sm->ent_row[lane] = a.T * a.K + lane;
       sm->ent_gate[lane] = 1.0f;
@@ -392,389 +377,378 @@ __device__ __forceinline__ void select_all(const Args& a, Small* sm) {
 
 // ---------------------------------------------------------------- work lists
 
-// First phase: units of eight gate and the eight matching up rows over all of
-// d. A CTA takes its share of the shared expert's units, then its share of the
-// routed ones (known after the selection).
-struct Units {
-  int sh0, sh1, r0, r1;
-  __device__ __forceinline__ int count() const { return (sh1 - sh0) + (r1 - r0); }
-};
-__device__ __forceinline__ void shared_units(const Args& a, Units& u) {
-  const int per = a.I >> 3;
-  u.sh0 = range_begin(blockIdx.x, per, gridDim.x);
-  u.sh1 = range_begin(blockIdx.x + 1, per, gridDim.x);
+// First phase: units of CH gate and the matching up rows over all of d, in slot
+// order, dealt to the CTAs in turn. The shared expert's come first (they are
+// known before the selection), and the slots are finished one after the other,
+// so that the second phase can start with the first slots while the last ones
+// are still on their way.
+__device__ __forceinline__ void unit_at(const Args& a, int unit, int& slot, int& ch) {
+  const int per = a.I / CH;
+  slot = unit / per;
+  ch = (unit - slot * per) * CH;
 }
-__device__ __forceinline__ void routed_units(const Args& a, int slots, Units& u) {
-  const int n = (slots - 1) * (a.I >> 3);
-  u.r0 = range_begin(blockIdx.x, n, gridDim.x);
-  u.r1 = range_begin(blockIdx.x + 1, n, gridDim.x);
-}
-__device__ __forceinline__ void unit_at(const Args& a, const Units& u, int i, int& slot, int& row) {
-  const int per = a.I >> 3;
-  if (i < u.sh1 - u.sh0) {
-    slot = 0;
-    row = (u.sh0 + i) * 8;
-  } else {
-    const int k = u.r0 + i - (u.sh1 - u.sh0);
-    slot = 1 + k / per;
-    row = (k % per) * 8;
+
+// The tokens' codes as operand tiles [d/128][rows8][128], 128-byte swizzle
+// (rows behind T stay unset), and their scales [d/128][16].
+__device__ __forceinline__ void stage_tokens(const Args& a, uint8_t* xh, float* xs) {
+  const int V = a.d >> 4, n = a.T * V;
+#pragma unroll 4
+  for (int o = threadIdx.x; o < n; o += CW * 32) {
+    const int t = o / V, v = o - t * V;
+    *reinterpret_cast<uint4*>(xh + (v >> 3) * (a.rows8 * 128) + t * 128 + (((v & 7) ^ (t & 7)) << 4)) =
+        __ldcg(reinterpret_cast<const uint4*>(a.xq) + o);
+  }
+  const int kb_d = a.d >> 7;
+  for (int i = threadIdx.x; i < kb_d * COLS; i += CW * 32) {
+    const int t = i & (COLS - 1);
+    xs[i] = t < a.T ? __ldcg(a.xs + t * kb_d + (i >> 4)) : 0.0f;
   }
 }
 
 // ---------------------------------------------------------------- kernel
 
-template <int NT>
 __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_constant__ Maps maps, const Args a) {
-  constexpr int EW = Shape<NT>::EW;
-  constexpr int RED = Shape<NT>::RED;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem;
-  uint8_t* xh = smem + static_cast<size_t>(a.stages) * STAGE;        // tokens' codes, then the H rows
-  float* red = reinterpret_cast<float*>(xh + a.xh_bytes);            // [EW][CW][8 NT][RCOL]
-  float* xs = red + EW * RED;                                        // [T][d/128]
-  Small* sm = reinterpret_cast<Small*>(xs + ((a.T * (a.d >> 7) + 3) & ~3));
+  uint8_t* xh = smem + static_cast<size_t>(a.stages) * STAGE;        // tokens' codes, then the H tiles
+  float* xs = reinterpret_cast<float*>(xh + a.xh_bytes);             // [d/128][16]
+  float* red = xs + (a.d >> 7) * COLS;                               // [EW][gate, up][16][CH]
+  Small* sm = reinterpret_cast<Small*>(red + EW * RED);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int xpitch = pitch_of(a.d), hpitch = pitch_of(a.hrec_bytes);
+  const int tile_bytes = a.rows8 * 128;                              // one block of the token operand
+  const int kb_d = a.d >> 7, kb_i = a.I >> 7;
   volatile int* abort = &sm->abort;
 
-  for (int i = threadIdx.x; i < MAX_SLOTS; i += THREADS) sm->mask[i] = 0u;
+  for (int i = threadIdx.x; i < MAX_N; i += THREADS) sm->mask[i] = 0u;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < MAX_STAGES; ++i) { mbar_init(&sm->full[i], 1); mbar_init(&sm->empty[i], CW); }
-    for (int i = 0; i < MAX_HBUF; ++i) { mbar_init(&sm->hfull[i], 1); mbar_init(&sm->hempty[i], CW); }
-    for (int i = 0; i < 4; ++i) { mbar_init(&sm->redfull[i], CW); mbar_init(&sm->redempty[i], 1); }
+    for (int i = 0; i < MAX_STAGES; ++i) { mbar_init(&sm->full[i], 1); mbar_init(&sm->empty[i], 1); }
+    for (int i = 0; i < MAX_HBUF; ++i) { mbar_init(&sm->hfull[i], 1); mbar_init(&sm->hempty[i], 3); }
+    for (int i = 0; i < BUFS; ++i) { mbar_init(&sm->tfull[i], 1); mbar_init(&sm->tempty[i], 2); }
+    for (int i = 0; i < EW; ++i) { mbar_init(&sm->redfull[i], 2); mbar_init(&sm->redempty[i], 1); }
     mbar_init(&sm->sel_ready, 1);
+    mbar_init(&sm->x_free, 1);
+    mbar_init(&sm->drained, 1);
     sm->abort = 0;
     fence_mbar_init();
   }
+  if (warp == CW + 1) {
+    tmem_alloc(&sm->tmem, TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm->tmem;
 
-  const int row0 = range_begin(blockIdx.x, a.d, gridDim.x);           // rows of W_down
+  const int row0 = range_begin(blockIdx.x, a.d, gridDim.x);           // the CTA's rows of W_down
   const int nrows = range_begin(blockIdx.x + 1, a.d, gridDim.x) - row0;
-  const int ntiles = (nrows + ROWS - 1) / ROWS;                       // the last one may be short
-  Units un;
-  shared_units(a, un);
+  const int per = a.I / CH;
 
   if (warp == CW) {
     // ------------------------------------------------------------ producer
-    int it = 0;
-    bool ok = true;
-    auto claim = [&](uint32_t bytes) -> uint8_t* {       // the next stage, expecting so many bytes
-      const int s = it % a.stages;
-      if (ok && it >= a.stages) ok = warp_wait(&sm->empty[s], ((it / a.stages) - 1) & 1, abort);
+    if (lane == 0) {
+      Cursor c;
+      c.lap = 1;                               // the first lap finds every stage empty
+      int issued = 0;
+      bool ok = true;
+      auto gate_up = [&](int unit) {
+        int slot, ch;
+        unit_at(a, unit, slot, ch);
+        const int row = (slot == 0 ? a.N_r : sm->slot_expert[slot]) * a.I + ch;
+        for (int k = 0; k < kb_d; k += SK) {
+          if (!(ok = mbar_wait(&sm->empty[c.i], c.lap, abort))) return;
+          uint64_t* bar = &sm->full[c.i];
+          uint8_t* dst = ring + c.i * STAGE;
+          mbar_arrive_expect_tx(bar, STAGE);   // d is a multiple of SK blocks
+          box_load(dst, &maps.gate, bar, row, k);
+          box_load(dst + STAGE / 2, &maps.up, bar, row, k);
+          ++issued;
+          c.next(a.stages);
+        }
+      };
+      int unit = blockIdx.x;
+      for (; ok && unit < per; unit += gridDim.x) gate_up(unit);
+      ok = ok && mbar_wait(&sm->sel_ready, 0, abort);
       if (ok) {
-        ++it;
-        if (lane == 0) mbar_arrive_expect_tx(&sm->full[s], bytes);
-        __syncwarp();
-      }
-      return ring + s * STAGE;
-    };
-    auto gate_up = [&](int i) {
-      int slot, row;
-      unit_at(a, un, i, slot, row);
-      row += (slot == 0 ? a.N_r : sm->slot_expert[slot]) * a.I;
-      for (int k = 0; k < a.d; k += KC) {
-        uint8_t* dst = claim(STAGE);
-        if (ok && lane < 2) box_load(dst + lane * (STAGE / 2), lane == 0 ? &maps.gate : &maps.up, &sm->full[(it - 1) % a.stages], row, k >> 7);
-      }
-    };
-    for (int i = 0; i < un.sh1 - un.sh0; ++i) gate_up(i);
-    ok = warp_wait(&sm->sel_ready, 0, abort) && ok;
-    if (ok) {
-      const int slots = sm->n_slots;
-      routed_units(a, slots, un);
-      for (int i = un.sh1 - un.sh0; i < un.count(); ++i) gate_up(i);
-      for (int si = 0; si < slots; ++si) {
-        const int row = sm->slot_expert[si] * a.d + row0;
-        for (int t = 0; t < ntiles; ++t) {
-          // a short tile is the boxes of its row count's bits, largest first
-          const int n = min(ROWS, nrows - t * ROWS);
-          const int bit = 4 - lane, above = lane > 0 && lane < 5 ? n & ~((2 << bit) - 1) : 0;
-          for (int k = 0; k < a.I; k += KC) {
-            uint8_t* dst = claim(n * KC);
-            if (ok && lane < 5 && ((n >> bit) & 1))
-              box_load(dst + above * KC, &maps.down[bit], &sm->full[(it - 1) % a.stages], row + t * ROWS + above, k >> 7);
+        const int slots = sm->n_slots;
+        for (; ok && unit < slots * per; unit += gridDim.x) gate_up(unit);
+        const CUtensorMap* down = &maps.down[nrows & 1];
+        for (int si = 0; ok && si < slots; ++si) {
+          const int row = sm->slot_expert[si] * a.d + row0;
+          for (int k = 0; k < kb_i; k += SK) {
+            if (!(ok = mbar_wait(&sm->empty[c.i], c.lap, abort))) break;
+            uint64_t* bar = &sm->full[c.i];
+            const int nk = min(SK, kb_i - k);
+            mbar_arrive_expect_tx(bar, nk * nrows * 128);
+            for (int j = 0; j < nk; ++j) tma_load_2d(ring + c.i * STAGE + j * TILE, down, bar, (k + j) * 128, row);
+            ++issued;
+            c.next(a.stages);
           }
         }
       }
+      // no copy may be in flight when the CTA ends
+      for (int j = max(0, issued - a.stages); j < issued; ++j)
+        mbar_wait(&sm->full[j % a.stages], (j / a.stages) & 1, abort);
     }
-    // no copy may be in flight when the CTA ends
-    for (int j = max(0, it - a.stages); j < it; ++j) mbar_wait(&sm->full[j % a.stages], (j / a.stages) & 1, &sm->abort);
-  } else if (warp > CW && warp <= CW + EW) {
-    // ------------------------------------------------------------ finishing warps
-    const int e = warp - CW - 1;
-    bool ok = warp_wait(&sm->sel_ready, 0, abort);
-    const int slots = ok ? sm->n_slots : 0;
-    if (ok) {
-      routed_units(a, slots, un);
-      for (int i = e, n = 0; i < un.count(); i += EW, ++n) {
-        if (!(ok = ok && warp_wait(&sm->redfull[e], n & 1, abort))) break;
-        int slot, row;
-        unit_at(a, un, i, slot, row);
-        const int first = sm->slot_start[slot], ntok = sm->slot_start[slot + 1] - first;
-        const float* p = red + e * RED;
-        float v[(8 * 8 * NT + 31) / 32];
+  } else if (warp == CW + 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = make_idesc(0, 0, 128, COLS);
+      bool ok = mbar_wait(&sm->sel_ready, 0, abort);
+      Cursor c, t;
+      t.lap = 1;
+      // one stage against nk blocks of the token operand at tok; the stage's blocks are `apart` bytes apart.
+      // MMAs into one sum wait for each other, so those of 2 QS sums are interleaved.
+      auto stage = [&](const uint8_t* tok, int nk, int apart) {
+        ok = ok && mbar_wait(&sm->tempty[t.i], t.lap, abort) && mbar_wait(&sm->full[c.i], c.lap, abort);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t ad = sw128_kmajor_desc(smem_u32(ring + c.i * STAGE));
+        const uint64_t bd = sw128_kmajor_desc(smem_u32(tok));
+        const uint32_t dt = tmem + t.i * BUF_COLS;
 #pragma unroll
-        for (int q = 0; q < 2 * NT; ++q) {
-          const int o = q * 32 + lane;
-          v[q] = 0.0f;
-          if (o < 8 * ntok) {
-            const float* c = p + (o >> 3) * RCOL + (o & 7);
-            float gt = 0.0f, up = 0.0f;
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int w = 0; w < CW; ++w) {
-              gt += c[w * 8 * NT * RCOL];
-              up += c[w * 8 * NT * RCOL + 8];
-            }
-            v[q] = __fdiv_rn(gt, 1.0f + expf(-gt)) * up;
+          for (int j = 0; j < SK; ++j)
+            if (j < nk)
+              umma_f8f6f4(dt + (j * QS + q % QS) * COLS, ad + ((j * apart) >> 4) + 2 * q,
+                          bd + ((j * tile_bytes) >> 4) + 2 * q, idesc, q >= QS);
+        umma_commit(&sm->empty[c.i]);
+        umma_commit(&sm->tfull[t.i]);
+        c.next(a.stages);
+        t.next(BUFS);
+      };
+      if (ok) {
+        const int slots = sm->n_slots;
+        for (int unit = blockIdx.x; ok && unit < slots * per; unit += gridDim.x)
+          for (int k = 0; ok && k < kb_d; k += SK) stage(xh + k * tile_bytes, SK, STAGE / 4);
+        umma_commit(&sm->x_free);
+        Cursor h;
+        for (int si = 0; ok && si < slots; ++si) {
+          ok = mbar_wait(&sm->hfull[h.i], h.lap, abort);
+          const uint8_t* hb = xh + h.i * a.hbuf_bytes;
+          for (int k = 0; ok && k < kb_i; k += SK) stage(hb + k * tile_bytes, min(SK, kb_i - k), TILE);
+          umma_commit(&sm->hempty[h.i]);
+          h.next(a.hbufs);
+        }
+      }
+      umma_commit(&sm->drained);                // no MMA may run when the TMEM is freed
+      mbar_wait(&sm->drained, 0, abort);
+    }
+  } else {
+    // ------------------------------------------------------------ router and selection
+    const int tid = threadIdx.x;
+    if (a.xq_ws != nullptr) quantise_u(a);
+    for (int e0 = blockIdx.x; e0 < a.N_r; e0 += 2 * gridDim.x)
+      affinities(a, sm, e0, e0 + static_cast<int>(gridDim.x) < a.N_r ? e0 + static_cast<int>(gridDim.x) : -1);
+    __threadfence();
+    named_bar_sync(1, CW * 32);
+    if (tid == 0) count_up(a.grid_ctr);
+    if (a.xq_ws == nullptr) stage_tokens(a, xh, xs);          // given by the caller: no need to wait
+    if (tid == 0) count_wait(a.grid_ctr, gridDim.x, abort);
+    named_bar_sync(1, CW * 32);
+    if (a.xq_ws != nullptr) stage_tokens(a, xh, xs);
+    fence_proxy_async_smem();
+    select_all(a, sm);
+    if (tid == 0) mbar_arrive(&sm->sel_ready);
+    const int slots = sm->n_slots, units = slots * per;
+
+    if (warp < 3) {
+      // ---------------------------------------------------------- sums of the partials: a thread owns a weight row
+      // first phase: gate rows are lanes 0..31 (warp 0), up rows lanes 64..95 (warp 2), the other lanes
+      // belong to the stage's other block; second phase: rows of W_down are lanes 0..63 (warps 0 and 1)
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+      bool ok = true;
+      Cursor t, e;
+      e.lap = 1;
+      float acc[COLS];
+      // the stage's partials, block j's in v[j * COLS ..]
+      auto partials = [&](float (&v)[SK * COLS]) {
+        ok = ok && warp_wait(&sm->tfull[t.i], t.lap, abort);
+        if (ok) {
+          uint32_t lo[32], hi[32];
+          tc_fence_after();
+          tmem_ld32_async(taddr + t.i * BUF_COLS, lo);
+          tmem_ld32_async(taddr + t.i * BUF_COLS + 32, hi);
+          tmem_wait_ld2(lo, hi);
+          tc_fence_before();
+#pragma unroll
+          for (int c = 0; c < COLS; ++c) {
+            v[c] = __uint_as_float(lo[c]) + __uint_as_float(lo[COLS + c]);
+            v[COLS + c] = __uint_as_float(hi[c]) + __uint_as_float(hi[COLS + c]);
           }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->tempty[t.i]);
+        t.next(BUFS);
+      };
+      if (warp == 1) {
+        const int mine = units > static_cast<int>(blockIdx.x) ? (units - blockIdx.x - 1) / gridDim.x + 1 : 0;
+        const int passed = mine * (kb_d / SK);
+        t.i = passed % BUFS;
+        t.lap = (passed / BUFS) & 1;
+      } else {
+        for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+          int slot, ch;
+          unit_at(a, unit, slot, ch);
+          const float* sw = (warp == 0 ? a.s_gate : a.s_up) +
+                            (static_cast<size_t>(sm->slot_expert[slot]) * kb_i + (ch >> 7)) * kb_d;
+#pragma unroll
+          for (int c = 0; c < COLS; ++c) acc[c] = 0.0f;
+          for (int k = 0; k < kb_d; k += SK) {
+            float w[SK], v[SK * COLS];
+#pragma unroll
+            for (int j = 0; j < SK; ++j) w[j] = __ldg(sw + k + j);
+            partials(v);
+            if (ok) {
+#pragma unroll
+              for (int j = 0; j < SK; ++j)
+#pragma unroll
+                for (int c = 0; c < COLS; c += 4) {
+                  const float4 x = *reinterpret_cast<const float4*>(xs + (k + j) * COLS + c);
+                  acc[c] = fmaf(v[j * COLS + c], x.x * w[j], acc[c]);
+                  acc[c + 1] = fmaf(v[j * COLS + c + 1], x.y * w[j], acc[c + 1]);
+                  acc[c + 2] = fmaf(v[j * COLS + c + 2], x.z * w[j], acc[c + 2]);
+                  acc[c + 3] = fmaf(v[j * COLS + c + 3], x.w * w[j], acc[c + 3]);
+                }
+            }
+          }
+          ok = ok && warp_wait(&sm->redempty[e.i], e.lap, abort);
+          if (ok) {
+            float* p = red + e.i * RED + (warp >> 1) * COLS * CH + lane;
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) p[c * CH] = acc[c];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm->redfull[e.i]);
+          e.next(EW);
+        }
+      }
+      if (warp < 2) {
+        // W_down: the CTA's rows over every slot
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) acc[c] = 0.0f;
+        const int r = warp * 32 + lane;
+        const int nb = (row0 + min(r, max(nrows - 1, 0))) >> 7;
+        Cursor h;
+        for (int si = 0; si < slots; ++si) {
+          const int ex = sm->slot_expert[si];
+          const uint32_t mask = si == 0 ? (1u << a.T) - 1u : sm->mask[ex];
+          const float* sw = a.s_down + (static_cast<size_t>(ex) * kb_d + nb) * kb_i;
+          ok = ok && warp_wait(&sm->hfull[h.i], h.lap, abort);
+          const float* hs = reinterpret_cast<const float*>(xh + h.i * a.hbuf_bytes + kb_i * tile_bytes);
+          for (int k = 0; k < kb_i; k += SK) {
+            const int nk = min(SK, kb_i - k);
+            float w[SK], v[SK * COLS];
+#pragma unroll
+            for (int j = 0; j < SK; ++j) w[j] = j < nk ? __ldg(sw + k + j) : 0.0f;
+            partials(v);
+            if (ok) {
+#pragma unroll
+              for (int j = 0; j < SK; ++j)
+                if (j < nk) {
+#pragma unroll
+                  for (int c = 0; c < COLS; ++c)
+                    if ((mask >> c) & 1u)          // others hold no token of this slot, and anything
+                      acc[c] = fmaf(v[j * COLS + c], hs[(k + j) * COLS + c] * w[j], acc[c]);
+                }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm->hempty[h.i]);
+          h.next(a.hbufs);
+        }
+        const uint16_t* base = a.base != nullptr ? a.base : a.u;
+        if (r < nrows) {
+#pragma unroll
+          for (int c = 0; c < COLS; ++c)
+            if (c < a.T) {
+              const size_t at = static_cast<size_t>(c) * a.d + row0 + r;
+              a.out[at] = float_to_bf16_bits(bf16_bits_to_float(base[at]) + acc[c]);
+            }
+        }
+      }
+    } else if (warp < 3 + EW) {
+      // ---------------------------------------------------------- finishing warps: SwiGLU, then the blocks' codes
+      const int e = warp - 3;
+      uint32_t lap = 0;
+      for (int unit = blockIdx.x + e * gridDim.x; unit < units; unit += EW * gridDim.x, lap ^= 1) {
+        if (!warp_wait(&sm->redfull[e], lap, abort)) break;
+        int slot, ch;
+        unit_at(a, unit, slot, ch);
+        const int first = sm->slot_start[slot], ntok = sm->slot_start[slot + 1] - first;
+        const float* p = red + e * RED + lane;
+        for (int j = 0; j < ntok; ++j) {
+          const int t = sm->ent_tok[first + j];
+          const float g = p[t * CH], u = p[(COLS + t) * CH];
+          a.act[static_cast<size_t>(sm->ent_row[first + j]) * a.I + ch + lane] = __fdiv_rn(g, 1.0f + expf(-g)) * u;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->redempty[e]);
-#pragma unroll
-        for (int q = 0; q < 2 * NT; ++q) {
-          const int o = q * 32 + lane;
-          if (o < 8 * ntok) a.act[static_cast<size_t>(sm->ent_row[first + (o >> 3)]) * a.I + row + (o & 7)] = v[q];
-        }
         // the warp that finishes a 128-block last quantises it
         __threadfence();
         __syncwarp();
         int last = 0;
-        const int blk = row >> 7;
-        if (lane == 0) last = atomicAdd(a.blk_ctr + slot * (a.I >> 7) + blk, 1) == 15;
+        const int blk = ch >> 7;
+        if (lane == 0) last = atomicAdd(a.blk_ctr + slot * kb_i + blk, 1) == 128 / CH - 1;
         if (__shfl_sync(0xffffffffu, last, 0)) {
           __threadfence();
           for (int j = 0; j < ntok; ++j) {
-            const int r = sm->ent_row[first + j];
+            const int r = sm->ent_row[first + j], t = sm->ent_tok[first + j];
             const float4 x = __ldcg(reinterpret_cast<const float4*>(a.act + static_cast<size_t>(r) * a.I + blk * 128) + lane);
             float amax = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
             const float s = tile_scale(amax);
-            uint8_t* rec = a.hrec + static_cast<size_t>(r) * a.hrec_bytes;
-            reinterpret_cast<uint32_t*>(rec + blk * 128)[lane] =
+            reinterpret_cast<uint32_t*>(a.hq + static_cast<size_t>(r) * a.I + blk * 128)[lane ^ ((t & 7) << 2)] =
                 e4m3x2(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s)) | (e4m3x2(__fdiv_rn(x.z, s), __fdiv_rn(x.w, s)) << 16);
-            if (lane == 0) reinterpret_cast<float*>(rec + a.I)[blk] = s;
+            if (lane == 0) a.hs[r * kb_i + blk] = s;
           }
+          fence_proxy_async_all();              // the codes are read by bulk copies
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) count_up(a.slot_done + slot);
         }
       }
-    }
-    asm volatile("fence.proxy.async;" ::: "memory");      // the records are read by bulk copies
-    __threadfence();
-    named_bar_sync(2, EW * 32);
-    if (e == 0) {
-      // -------------------------------------------------------- loader of H
-      int seen = 0;
-      if (lane == 0) {
-        grid_arrive(a.grid_ctr + 32);
-        seen = grid_wait(a.grid_ctr + 32, gridDim.x, abort);
-      }
-      ok = __shfl_sync(0xffffffffu, seen, 0) != 0 && ok;
-      asm volatile("fence.proxy.async;" ::: "memory");
+    } else if (warp == 3 + EW) {
+      // ---------------------------------------------------------- loader of the H tiles, over the tokens' operand
+      bool ok = warp_wait(&sm->x_free, 0, abort);
+      Cursor h;
+      h.lap = 1;
       int si = 0;
       for (; ok && si < slots; ++si) {
-        const int bf = si % a.hbufs;
-        if (si >= a.hbufs && !(ok = warp_wait(&sm->hempty[bf], ((si / a.hbufs) - 1) & 1, abort))) break;
+        if (!(ok = warp_wait(&sm->hempty[h.i], h.lap, abort))) break;
+        int seen = 0;
+        if (lane == 0) seen = count_wait(a.slot_done + si, kb_i, abort);
+        if (!(ok = __shfl_sync(0xffffffffu, seen, 0) != 0)) break;
+        fence_proxy_async_all();
         const int first = sm->slot_start[si], ntok = sm->slot_start[si + 1] - first;
-        if (lane == 0) mbar_arrive_expect_tx(&sm->hfull[bf], ntok * a.hrec_bytes);
-        __syncwarp();
-        if (lane < ntok)
-          bulk_load(xh + (static_cast<size_t>(bf) * a.T + lane) * hpitch,
-                    a.hrec + static_cast<size_t>(sm->ent_row[first + lane]) * a.hrec_bytes, a.hrec_bytes, &sm->hfull[bf]);
-      }
-      for (int j = max(0, si - a.hbufs); j < si; ++j) mbar_wait(&sm->hfull[j % a.hbufs], (j / a.hbufs) & 1, &sm->abort);
-    }
-  } else if (warp < CW) {
-    // ------------------------------------------------------------ multiplying warps
-    const int tid = threadIdx.x;
-    const int g = lane >> 2, q4 = lane & 3;
-    if (a.xq_ws != nullptr) quantise_u(a);
-    for (int e0 = blockIdx.x; e0 < a.N_r; e0 += 2 * gridDim.x) {
-      const int e1 = e0 + static_cast<int>(gridDim.x) < a.N_r ? e0 + static_cast<int>(gridDim.x) : -1;
-      for (int t0 = 0; t0 < a.T; t0 += 8) affinities(a, sm, e0, e1, t0);
-    }
-    __threadfence();
-    named_bar_sync(1, CW * 32);
-    if (tid == 0) {
-      grid_arrive(a.grid_ctr);
-      grid_wait(a.grid_ctr, gridDim.x, abort);
-    }
-    named_bar_sync(1, CW * 32);
-    select_all(a, sm);
-    // the tokens' codes and scales
-    for (int t = 0; t < a.T; ++t)
-      for (int v = tid; v < (a.d >> 4); v += CW * 32)
-        *reinterpret_cast<uint4*>(xh + t * xpitch + v * 16) =
-            __ldcg(reinterpret_cast<const uint4*>(a.xq + static_cast<size_t>(t) * a.d) + v);
-    for (int i = tid; i < a.T * (a.d >> 7); i += CW * 32) xs[i] = __ldcg(a.xs + i);
-    named_bar_sync(1, CW * 32);
-    if (tid == 0) mbar_arrive(&sm->sel_ready);
-
-    const int slots = sm->n_slots;
-    routed_units(a, slots, un);
-    const int kb_d = a.d >> 7, kb_i = a.I >> 7;
-    int it = 0;
-    bool ok = true;
-    for (int i = 0; i < un.count(); ++i) {
-      int slot, row;
-      unit_at(a, un, i, slot, row);
-      const int ex = sm->slot_expert[slot];
-      const int first = sm->slot_start[slot], ntok = sm->slot_start[slot + 1] - first;
-      const float* sg = a.s_gate + (static_cast<size_t>(ex) * kb_i + (row >> 7)) * kb_d;
-      const float* su = a.s_up + (static_cast<size_t>(ex) * kb_i + (row >> 7)) * kb_d;
-      float acc[NT][4];
-      int tok[NT], c0[NT], c1[NT];           // the lane's B column, and its two result columns
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
-        tok[n] = sm->ent_tok[first + min(n * 8 + g, ntok - 1)];
-        c0[n] = sm->ent_tok[first + min(n * 8 + 2 * q4, ntok - 1)] * kb_d;
-        c1[n] = sm->ent_tok[first + min(n * 8 + 2 * q4 + 1, ntok - 1)] * kb_d;
-      }
-      for (int k0 = 0; k0 < a.d; k0 += KC, ++it) {
-        const int s = it % a.stages;
-        const int kb = (k0 >> 7) + warp;
-        const bool mine = kb < kb_d;
-        const float fg = mine ? __ldg(sg + kb) : 0.0f, fu = mine ? __ldg(su + kb) : 0.0f;
-        ok = ok && warp_wait(&sm->full[s], (it / a.stages) & 1, abort);
-        if (ok && mine) {
-          const uint8_t* p = ring + s * STAGE + warp * 1024 + g * 128;
-          const Frag r0 = weight_frag(p, q4), r8 = weight_frag(p + STAGE / 2, q4);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (n * 8 < ntok) {
-              const Frag x = token_frag(xh + tok[n] * xpitch + kb * 128 + q4 * 32);
-              float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              block_product(c, r0, r8, x);
-              const float x0 = xs[c0[n] + kb], x1 = xs[c1[n] + kb];
-              acc[n][0] = fmaf(c[0], x0 * fg, acc[n][0]);
-              acc[n][1] = fmaf(c[1], x1 * fg, acc[n][1]);
-              acc[n][2] = fmaf(c[2], x0 * fu, acc[n][2]);
-              acc[n][3] = fmaf(c[3], x1 * fu, acc[n][3]);
-            }
-          }
+        uint8_t* hb = xh + h.i * a.hbuf_bytes;
+        float* hs = reinterpret_cast<float*>(hb + kb_i * tile_bytes);
+        for (int o = lane; o < ntok * kb_i; o += 32) {
+          const int j = o / kb_i, k = o - j * kb_i;
+          hs[k * COLS + sm->ent_tok[first + j]] = __ldcg(a.hs + sm->ent_row[first + j] * kb_i + k) * sm->ent_gate[first + j];
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->empty[s]);
-      }
-      const int e = i % EW, use = i / EW;
-      if (use > 0) ok = ok && warp_wait(&sm->redempty[e], (use - 1) & 1, abort);
-      if (ok) {
-        float* r = red + e * RED + warp * 8 * NT * RCOL;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float* c = r + (n * 8 + 2 * q4) * RCOL + g;
-          c[0] = acc[n][0];
-          c[RCOL] = acc[n][1];
-          c[8] = acc[n][2];
-          c[RCOL + 8] = acc[n][3];
+        if (lane == 0) mbar_arrive_expect_tx(&sm->hfull[h.i], ntok * a.I);
+        __syncwarp();
+        for (int o = lane; o < ntok * kb_i; o += 32) {
+          const int j = o / kb_i, k = o - j * kb_i;
+          bulk_load(hb + k * tile_bytes + sm->ent_tok[first + j] * 128,
+                    a.hq + static_cast<size_t>(sm->ent_row[first + j]) * a.I + k * 128, 128, &sm->hfull[h.i]);
         }
+        h.next(a.hbufs);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->redfull[e]);
-    }
-
-    // ---------------------------------------------------------- W_down
-    float acc[MAX_TILES][NT][4];
-#pragma unroll
-    for (int t = 0; t < MAX_TILES; ++t)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[t][n][j] = 0.0f;
-    for (int si = 0; si < slots; ++si) {
-      const int bf = si % a.hbufs;
-      ok = ok && warp_wait(&sm->hfull[bf], (si / a.hbufs) & 1, abort);
-      const int ex = sm->slot_expert[si];
-      const int first = sm->slot_start[si];
-      const uint32_t mask = si == 0 ? (1u << a.T) - 1u : sm->mask[ex];
-      const uint8_t* hb = xh + static_cast<size_t>(bf) * a.T * hpitch;
-      const uint8_t* col[NT];                // the lane's B column: its token's row of H, or none
-      const float *h0[NT], *h1[NT];          // scales of the two result columns
-      float g0[NT], g1[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        auto at = [&](int c) { return (mask >> c) & 1u ? __popc(mask & ((1u << c) - 1u)) : -1; };
-        const int jb = at(n * 8 + g), j0 = at(n * 8 + 2 * q4), j1 = at(n * 8 + 2 * q4 + 1);
-        col[n] = jb < 0 ? nullptr : hb + jb * hpitch;
-        h0[n] = j0 < 0 ? nullptr : reinterpret_cast<const float*>(hb + j0 * hpitch + a.I);
-        h1[n] = j1 < 0 ? nullptr : reinterpret_cast<const float*>(hb + j1 * hpitch + a.I);
-        g0[n] = j0 < 0 ? 0.0f : sm->ent_gate[first + j0];
-        g1[n] = j1 < 0 ? 0.0f : sm->ent_gate[first + j1];
-      }
-#pragma unroll
-      for (int t = 0; t < MAX_TILES; ++t) {
-        if (t >= ntiles) continue;
-        const int nr = min(ROWS, nrows - t * ROWS);
-        const int ra = min(g, nr - 1), rb = min(g + 8, nr - 1);          // rows past a short tile repeat its last
-        const int oa = box_offset(ra, nr) + warp * box_rows(ra, nr) * 128, ob = box_offset(rb, nr) + warp * box_rows(rb, nr) * 128;
-        const int n0 = (row0 + t * ROWS + ra) >> 7, n8 = (row0 + t * ROWS + rb) >> 7;
-        const float* s0 = a.s_down + (static_cast<size_t>(ex) * kb_d + n0) * kb_i;
-        const float* s8 = a.s_down + (static_cast<size_t>(ex) * kb_d + n8) * kb_i;
-        for (int k0 = 0; k0 < a.I; k0 += KC, ++it) {
-          const int s = it % a.stages;
-          const int kb = (k0 >> 7) + warp;
-          const bool mine = kb < kb_i;
-          const float f0 = mine ? __ldg(s0 + kb) : 0.0f, f8 = mine ? __ldg(s8 + kb) : 0.0f;
-          ok = ok && warp_wait(&sm->full[s], (it / a.stages) & 1, abort);
-          if (ok && mine) {
-            const uint8_t* p = ring + s * STAGE;
-            const Frag r0 = weight_frag(p + oa, q4), r8 = weight_frag(p + ob, q4);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              if ((mask >> (n * 8)) & 0xFFu) {
-                Frag x = {{0, 0, 0, 0, 0, 0, 0, 0}};
-                if (col[n] != nullptr) x = token_frag(col[n] + kb * 128 + q4 * 32);
-                __syncwarp();
-                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                block_product(c, r0, r8, x);
-                if (h0[n] != nullptr) {      // a column without a token adds nothing, whatever the weights hold
-                  const float x0 = h0[n][kb] * g0[n];
-                  acc[t][n][0] = fmaf(c[0], x0 * f0, acc[t][n][0]);
-                  acc[t][n][2] = fmaf(c[2], x0 * f8, acc[t][n][2]);
-                }
-                if (h1[n] != nullptr) {
-                  const float x1 = h1[n][kb] * g1[n];
-                  acc[t][n][1] = fmaf(c[1], x1 * f0, acc[t][n][1]);
-                  acc[t][n][3] = fmaf(c[3], x1 * f8, acc[t][n][3]);
-                }
-              }
-            }
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm->empty[s]);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->hempty[bf]);
-    }
-    // the warps' sums meet in the ring, which is empty now
-    named_bar_sync(1, CW * 32);
-    float* fin = reinterpret_cast<float*>(ring);             // [CW][8 NT][64]
-#pragma unroll
-    for (int t = 0; t < MAX_TILES; ++t)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float* c = fin + (warp * 8 * NT + n * 8 + 2 * q4) * 64 + t * 16 + g;
-        c[0] = acc[t][n][0];
-        c[64] = acc[t][n][1];
-        c[8] = acc[t][n][2];
-        c[72] = acc[t][n][3];
-      }
-    named_bar_sync(1, CW * 32);
-    const uint16_t* base = a.base != nullptr ? a.base : a.u;
-    for (int o = tid; o < a.T * 64; o += CW * 32) {
-      const int t = o >> 6, r = o & 63;
-      if (r >= nrows) continue;
-      float v = 0.0f;
-#pragma unroll
-      for (int w = 0; w < CW; ++w) v += fin[(w * 8 * NT + t) * 64 + r];
-      const size_t at = static_cast<size_t>(t) * a.d + row0 + r;
-      a.out[at] = float_to_bf16_bits(bf16_bits_to_float(base[at]) + v);
+      for (int j = max(0, si - a.hbufs); j < si; ++j) mbar_wait(&sm->hfull[j % a.hbufs], (j / a.hbufs) & 1, abort);
     }
   }
+  tc_fence_before();
   __syncthreads();
+  if (warp == CW + 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
 }
 
 // ---------------------------------------------------------------- host
@@ -782,71 +756,40 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
 inline size_t round_up(size_t n, size_t m) { return (n + m - 1) / m * m; }
 
 struct Layout {
-  size_t ctr_bytes, scores, xq, xs, act, hrec, total;
-  int hrec_bytes;
+  size_t slots, ctr_bytes, scores, xq, xs, act, hq, hs, total;
 };
 inline Layout layout(int T, int d, int N_r, int K_r, int I) {
   Layout l;
   const size_t P = static_cast<size_t>(T) * K_r + T;
-  const size_t slots = (static_cast<size_t>(T) * K_r < static_cast<size_t>(N_r) ? T * K_r : N_r) + 1;
-  l.ctr_bytes = 256 + slots * (I / 128) * 4;
+  const size_t slots = (T * K_r < N_r ? T * K_r : N_r) + 1;
+  l.slots = slots;
+  l.ctr_bytes = 128 + slots * 4 + slots * (I / 128) * 4;
   l.scores = round_up(l.ctr_bytes, 256);
-  l.xq = round_up(l.scores + static_cast<size_t>(T) * N_r * 4, 256);
+  l.xq = round_up(l.scores + static_cast<size_t>(T) * N_r * 8, 256);
   l.xs = round_up(l.xq + static_cast<size_t>(T) * d, 256);
   l.act = round_up(l.xs + static_cast<size_t>(T) * (d / 128) * 4, 256);
-  l.hrec = round_up(l.act + P * I * 4, 256);
-  l.hrec_bytes = static_cast<int>(round_up(I + I / 128 * 4, 16));
-  l.total = l.hrec + P * l.hrec_bytes;
+  l.hq = round_up(l.act + P * I * 4, 256);
+  l.hs = round_up(l.hq + P * I, 256);
+  l.total = round_up(l.hs + P * (I / 128) * 4, 256);
   return l;
 }
 
-inline bool sizes_supported(int T, int d, int N_r, int K_r, int I) {
-  return T <= MAX_T && K_r >= 1 && K_r <= MAX_K && K_r <= N_r && N_r <= MAX_N && d % 256 == 0 && d <= 8192 &&
-         I % 128 == 0 && I <= 8192;
-}
-
-// [rows][cols] codes as (128, rows, cols / 128), boxes of R rows by KC / 128 blocks.
-inline int make_map(CUtensorMap* m, const void* base, size_t rows, int cols, int R) {
+// [rows][cols] codes as (128, rows, cols / 128), boxes of CH rows by SK blocks.
+inline int make_map(CUtensorMap* m, const void* base, size_t rows, int cols) {
   auto enc = tensor_map_encoder();
   if (!enc) return record_failure(MOE_ERR_CUDA, "cuTensorMapEncodeTiled", "entry point not found");
   cuuint64_t dims[3] = {128, rows, static_cast<cuuint64_t>(cols / 128)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols), 128};
-  cuuint32_t box[3] = {128, static_cast<cuuint32_t>(R), KC / 128}, one[3] = {1, 1, 1};
+  cuuint32_t box[3] = {128, CH, SK}, one[3] = {1, 1, 1};
   const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, one,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? MOE_OK : record_failure(MOE_ERR_CUDA, "cuTensorMapEncodeTiled", "few tokens: weight map");
 }
 
-template <int NT>
-int launch(const Maps& maps, Args& a, const DeviceInfo& di, cudaStream_t s) {
-  const int xpitch = pitch_of(a.d), hpitch = pitch_of(a.hrec_bytes);
-  const int one = a.T * hpitch;
-  int xh = a.T * xpitch > 2 * one ? a.T * xpitch : 2 * one;
-  a.hbufs = xh / one;
-  if (a.hbufs > MAX_HBUF) a.hbufs = MAX_HBUF;
-  a.xh_bytes = static_cast<int>(round_up(xh, 16));
-  const size_t rest = a.xh_bytes + Shape<NT>::EW * Shape<NT>::RED * 4 + round_up(a.T * (a.d / 128) * 4, 16) + sizeof(Small);
-  if (rest + 3 * STAGE > SMEM_MAX)
-    return record_failure(MOE_ERR_UNSUPPORTED, "moe_few_tokens", "T * d and T * I do not fit shared memory");
-  a.stages = static_cast<int>((SMEM_MAX - rest) / STAGE);
-  if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
-  const size_t smem = rest + static_cast<size_t>(a.stages) * STAGE;
-  auto k = few_tokens_kernel<NT>;
-  if (int st = cuda_status(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)),
-                           "few tokens: smem attribute"))
-    return st;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(di.sm_count);
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeCooperative;       // every CTA waits for every other twice
-  at[0].val.cooperative = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, k, maps, static_cast<const Args>(a)), "few tokens: launch");
+inline bool sizes_supported(int T, int d, int N_r, int K_r, int I) {
+  return T <= MAX_T && K_r >= 1 && K_r <= MAX_K && K_r <= N_r && N_r <= MAX_N && d % 256 == 0 && d <= MAX_D &&
+         I % 128 == 0 && I <= MAX_D;
 }
 
 }  // namespace few
@@ -880,8 +823,9 @@ extern "C" int moe_few_tokens(const uint16_t* u, const uint8_t* xq, const float*
   MOE_CHECK_ARG(all % 16 == 0);
   DeviceInfo di;
   if (int st = device_info(&di)) return st;
-  if (di.sm_count < 1 || (d + di.sm_count - 1) / di.sm_count > MAX_TILES * ROWS)
-    return record_failure(MOE_ERR_UNSUPPORTED, "moe_few_tokens", "too few SMs for d");
+  const int G = di.sm_count;
+  if ((d + G - 1) / G > LIVE) return record_failure(MOE_ERR_UNSUPPORTED, "moe_few_tokens", "too few SMs for d");
+
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   Args a{};
   a.u = u; a.base = base; a.e = e; a.b = b;
@@ -892,18 +836,51 @@ extern "C" int moe_few_tokens(const uint16_t* u, const uint8_t* xq, const float*
   a.s_gate = s_gate; a.s_up = s_up; a.s_down = s_down;
   a.out = out; a.topk_idx = topk_idx; a.gates = gates; a.counts = counts;
   a.grid_ctr = reinterpret_cast<unsigned*>(ws);
-  a.blk_ctr = reinterpret_cast<int*>(ws + 256);
-  a.scores = reinterpret_cast<float*>(ws + l.scores);
+  a.slot_done = reinterpret_cast<unsigned*>(ws + 128);
+  a.blk_ctr = reinterpret_cast<int*>(ws + 128 + l.slots * 4);
+  a.scores = reinterpret_cast<float2*>(ws + l.scores);
   a.act = reinterpret_cast<float*>(ws + l.act);
-  a.hrec = ws + l.hrec;
-  a.hrec_bytes = l.hrec_bytes;
+  a.hq = ws + l.hq;
+  a.hs = reinterpret_cast<float*>(ws + l.hs);
   a.T = T; a.d = d; a.N_r = N_r; a.K = K_r; a.I = I;
+
+  // shared memory: the token operand (8 or 16 rows a block) and the H tiles
+  // take turns in one region; the ring gets what is left
+  a.rows8 = T <= 8 ? 8 : 16;
+  const int x_bytes = (d / 128) * a.rows8 * 128;
+  a.hbuf_bytes = static_cast<int>(round_up((I / 128) * (a.rows8 * 128 + COLS * 4), 1024));
+  a.xh_bytes = x_bytes > a.hbuf_bytes ? x_bytes : a.hbuf_bytes;
+  if (a.xh_bytes < 2 * a.hbuf_bytes && 2 * a.hbuf_bytes <= 96 * 1024) a.xh_bytes = 2 * a.hbuf_bytes;
+  a.hbufs = a.xh_bytes / a.hbuf_bytes;
+  if (a.hbufs > MAX_HBUF) a.hbufs = MAX_HBUF;
+  const size_t rest = a.xh_bytes + (d / 128) * COLS * 4 + EW * RED * 4 + sizeof(Small);
+  a.stages = static_cast<int>((SMEM_MAX - rest) / STAGE);
+  if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
+  const size_t smem = rest + static_cast<size_t>(a.stages) * STAGE;
+
   Maps maps;
-  const size_t G = static_cast<size_t>(N_r) + 1;
-  if (int st = make_map(&maps.gate, w_gate, G * I, d, 8)) return st;
-  if (int st = make_map(&maps.up, w_up, G * I, d, 8)) return st;
-  for (int i = 0; i < 5; ++i)
-    if (int st = make_map(&maps.down[i], w_down, G * d, I, 1 << i)) return st;
+  const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const uint64_t slots = static_cast<uint64_t>(N_r) + 1;
+  if (int st = make_map(&maps.gate, w_gate, slots * I, d)) return st;
+  if (int st = make_map(&maps.up, w_up, slots * I, d)) return st;
+  for (int i = 0; i < 2; ++i) {          // CTAs own d / G rows or one more: one count is even, one odd
+    const int n = d / G + ((d / G) % 2 == i ? 0 : 1);
+    if (int st = make_tmap_2d(&maps.down[i], w_down, U8, 1, slots * d, I, n > 0 ? n : 1, 128)) return st;
+  }
   if (int st = cuda_status(cudaMemsetAsync(ws, 0, l.ctr_bytes, s), "few tokens: counters")) return st;
-  return T <= 8 ? launch<1>(maps, a, di, s) : launch<2>(maps, a, di, s);
+  if (int st = cuda_status(cudaFuncSetAttribute(few_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                static_cast<int>(smem)),
+                           "few tokens: smem attribute"))
+    return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(G);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeCooperative;       // every CTA waits for every other twice
+  at[0].val.cooperative = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, few_tokens_kernel, maps, static_cast<const Args>(a)), "few tokens: launch");
 }

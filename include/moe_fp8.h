@@ -535,10 +535,8 @@ MOE_API int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int stream_i
  * CTAs wait for one another, so two calls that share a workspace must not
  * overlap (calls with workspaces of their own may). Results do not depend on
  * the schedule. T = 0 only zeroes counts.
- * Limits: K_r <= 16, K_r <= N_r <= 256, d a multiple of 256 up to 8192, I a
- * multiple of 128 up to 8192, and T rows of d, or 2 T rows of I, within shared
- * memory beside three stages of weights (else MOE_ERR_UNSUPPORTED: at T = 16,
- * I up to 4096; at T = 8, any).
+ * Limits: K_r <= 16, K_r <= N_r <= 256, d a multiple of 256 up to 8192 (and up
+ * to 64 times the SM count), I a multiple of 128 up to 8192.
  * moe_few_tokens_workspace returns 0 for sizes outside the limits.
  */
 MOE_API size_t moe_few_tokens_workspace(int T, int d, int N_r, int K_r, int I);
