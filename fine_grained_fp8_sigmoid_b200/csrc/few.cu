@@ -9,13 +9,17 @@
 // expert while the router runs and with W_down while the last intermediate rows
 // are written.
 //
-// Products: weight rows are the MMA's M side (128, of which 64 are live: a unit
-// of the first phase is 32 gate and the matching 32 up rows, the second phase
-// has the CTA's own d / SMs rows of W_down), tokens its N side (16, those
-// behind T ignored). The 64 live rows are a choice of balance: one token has 9
-// experts, 576 such units for 148 SMs (0.97 of them busy in the last round),
-// and MMAs with half of their rows dead still take under half of the time that
-// their 8 KB of weights take to arrive.
+// Products: weight rows are the MMA's M side, tokens its N side. A stage of the
+// ring holds two 128-channel blocks of 64 weight rows, and one MMA takes both:
+// its 128 rows are the 64 rows of either block, its columns the R token rows
+// (8 or 16) of either block's activations, and of the four quarters of the
+// result the two that pair a block with itself are read. That keeps every
+// weight row live and halves the number of MMAs, whose issue (about 70 cycles
+// each, whatever their shape) would otherwise pace the kernel: 8 KB of weights
+// arrive in about 340 cycles. 64 rows is a choice of balance: one token has 9
+// experts, 576 units of 32 gate and 32 up rows for 148 SMs (0.97 of them busy
+// in the last round), and in the second phase every CTA has its own d / SMs
+// rows of W_down, at most 64, over all slots.
 #include "host.cuh"
 
 namespace moe {
@@ -28,7 +32,7 @@ constexpr int MAX_SLOTS = MAX_N + 1;
 constexpr int MAX_ENTRIES = MAX_T * MAX_K + MAX_T;
 constexpr int MAX_D = 8192;
 constexpr int CW = 8;                        // warps of the router and the selection
-constexpr int EW = 3;                        // of them, finishing warps of the first phase
+constexpr int PW = 4;                        // of them, warps that add up partials, one per 32 TMEM lanes
 constexpr int THREADS = (CW + 2) * 32;       // and the producer, the MMA issuer
 constexpr int CH = 32;                       // intermediate channels of a unit
 constexpr int LIVE = 64;                     // live weight rows of a tile
@@ -37,12 +41,9 @@ constexpr int TILE = LIVE * 128;             // bytes of one block of a stage
 constexpr int STAGE = SK * TILE;
 constexpr int MAX_STAGES = 12;
 constexpr int MAX_HBUF = 4;
-constexpr int COLS = 16;                     // MMA columns: tokens
+constexpr int COLS = 16;                     // a row of the scale tables
 constexpr int QS = 2;                        // sums of a block's four K = 32 steps: even and odd ones apart
-constexpr int BUF_COLS = SK * QS * COLS;     // TMEM columns of a stage's partials
-constexpr int BUFS = 8;
-constexpr int TMEM_COLS = BUFS * BUF_COLS;
-constexpr int RED = 2 * COLS * CH;           // floats of one unit's sums
+constexpr int BUFS = 8;                      // stages' partials in TMEM
 constexpr int SMEM_MAX = 227 * 1024;
 
 // Maps of the weights, rows [slot * rows] of codes, boxes of 128 channels by:
@@ -60,6 +61,7 @@ struct Args {
   const float* xs;
   uint8_t* xq_ws;           // not NULL: quantise u into the workspace
   float* xs_ws;
+  const uint8_t *w_gate_shared, *w_up_shared;
   const float *s_gate, *s_up, *s_down;
   uint16_t* out;
   int32_t* topk_idx;
@@ -70,11 +72,21 @@ struct Args {
   int* blk_ctr;             // [slot][I/128]: finished units of a block
   float2* scores;           // [T][N_r] key s + b, affinity s
   float* act;               // [T*K + T][I] silu(G) U
-  uint8_t* hq;              // [T*K + T][I] its codes, 16-byte words swizzled by token
+  uint8_t* hq;              // [T*K + T][I] its codes, 16-byte words swizzled by place in the slot
   float* hs;                // [T*K + T][I/128]
   int T, d, N_r, K, I;
-  int rows8;                // token rows of an operand tile: 8 or 16
   int stages, hbufs, xh_bytes, hbuf_bytes;
+};
+
+// R: token rows of an operand tile (T rounded up to 8).
+template <int R>
+struct Shape {
+  static constexpr int EW = R == 8 ? 3 : 2;                 // finishing warps of the first phase
+  static constexpr int N = SK * R;                          // MMA columns: token rows of the stage's two blocks
+  static constexpr int BUF_COLS = QS * N;                   // TMEM columns of a stage's partials
+  static constexpr int TMEM_COLS = BUFS * BUF_COLS;
+  static constexpr int RED = PW * R * CH;                   // floats of one unit's sums
+  static constexpr int FLOATS = EW * RED + PW * R * 32;     // with the outputs' sums
 };
 
 // Shared memory behind the dynamic regions.
@@ -82,7 +94,7 @@ struct Small {
   uint64_t full[MAX_STAGES], empty[MAX_STAGES];
   uint64_t hfull[MAX_HBUF], hempty[MAX_HBUF];
   uint64_t tfull[BUFS], tempty[BUFS];
-  uint64_t redfull[EW], redempty[EW];
+  uint64_t redfull[3], redempty[3];
   uint64_t sel_ready, x_free, drained;
   uint32_t tmem;
   int abort;
@@ -124,6 +136,26 @@ __device__ __forceinline__ void box_load(void* dst, const CUtensorMap* m, uint64
           smem_u32(dst)),
       "l"(m), "r"(smem_u32(bar)), "r"(0), "r"(row), "r"(block)
       : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+// Issues a read of NC consecutive FP32 columns of the thread's TMEM lane.
+template <int NC>
+__device__ __forceinline__ void tmem_ld_async(uint32_t taddr, uint32_t* r) {
+  static_assert(NC == 2 || NC == 4 || NC == 8 || NC == 16, "columns");
+  if constexpr (NC == 2) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr));
+  } else if constexpr (NC == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
+  } else {
+#pragma unroll
+    for (int i = 0; i < NC; i += 8) tmem_ld8_async(taddr + i, r + i);
+  }
 }
 
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
@@ -173,60 +205,84 @@ __device__ __forceinline__ void to_double8(const uint4 v, double (&f)[8]) {
   }
 }
 
+// TC: token capacity. Up to LEAD tokens load everything ahead (one latency).
+constexpr int LEAD = 4;
+template <int TC>
 __device__ __forceinline__ void affinities(const Args& a, Small* sm, int e0, int e1) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  double acc[32];                            // [expert][token]
+  double acc[2 * TC];                        // [expert][token]
 #pragma unroll
-  for (int i = 0; i < 32; ++i) acc[i] = 0.0;
-  const int V = a.d >> 3;
+  for (int i = 0; i < 2 * TC; ++i) acc[i] = 0.0;
+  const int V = a.d >> 3;                    // at most four runs of 8 channels a thread
   const uint4* r0 = reinterpret_cast<const uint4*>(a.e + static_cast<size_t>(e0) * a.d);
   const uint4* r1 = reinterpret_cast<const uint4*>(a.e + static_cast<size_t>(e1 < 0 ? e0 : e1) * a.d);
   const uint4* ru = reinterpret_cast<const uint4*>(a.u);
-  int v = tid;
-  uint4 n0 = make_uint4(0, 0, 0, 0), n1 = n0;
-  if (v < V) { n0 = __ldg(r0 + v); n1 = __ldg(r1 + v); }
-  for (; v < V; v += CW * 32) {
-    double w0[8], w1[8];
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  auto add = [&](const uint4 n0, const uint4 n1, const uint4* x, int t0, int n) {
+    double w0[8], w1[8], f[8];
     to_double8(n0, w0);
     to_double8(n1, w1);
-    if (v + CW * 32 < V) { n0 = __ldg(r0 + v + CW * 32); n1 = __ldg(r1 + v + CW * 32); }
 #pragma unroll
-    for (int t0 = 0; t0 < MAX_T; t0 += 8) {
-      uint4 x[8];                            // eight tokens' runs at once: one latency
+    for (int t = 0; t < (TC < 8 ? TC : 8); ++t)
+      if (t < n) {
+        to_double8(x[t], f);
 #pragma unroll
-      for (int t = 0; t < 8; ++t)
-        if (t0 + t < a.T) x[t] = __ldg(ru + static_cast<size_t>(t0 + t) * V + v);
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-        if (t0 + t < a.T) {
-          double f[8];
-          to_double8(x[t], f);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            acc[t0 + t] = fma(f[j], w0[j], acc[t0 + t]);
-            acc[MAX_T + t0 + t] = fma(f[j], w1[j], acc[MAX_T + t0 + t]);
-          }
+        for (int j = 0; j < 8; ++j) {
+          acc[t0 + t] = fma(f[j], w0[j], acc[t0 + t]);
+          acc[TC + t0 + t] = fma(f[j], w1[j], acc[TC + t0 + t]);
         }
+      }
+  };
+  if constexpr (TC <= LEAD) {
+    uint4 we[4][2], x[4][TC];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int v = tid + i * CW * 32;
+      we[i][0] = v < V ? __ldg(r0 + v) : zero;
+      we[i][1] = v < V ? __ldg(r1 + v) : zero;
+#pragma unroll
+      for (int t = 0; t < TC; ++t) x[i][t] = v < V && t < a.T ? __ldg(ru + static_cast<size_t>(t) * V + v) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) add(we[i][0], we[i][1], x[i], 0, a.T);
+  } else {
+    int v = tid;
+    uint4 n0 = v < V ? __ldg(r0 + v) : zero, n1 = v < V ? __ldg(r1 + v) : zero;
+    for (; v < V; v += CW * 32) {
+      const uint4 c0 = n0, c1 = n1;
+      if (v + CW * 32 < V) { n0 = __ldg(r0 + v + CW * 32); n1 = __ldg(r1 + v + CW * 32); }
+#pragma unroll
+      for (int t0 = 0; t0 < TC; t0 += 8) {
+        uint4 x[8];                          // eight tokens' runs at once
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+          if (t0 + t < a.T) x[t] = __ldg(ru + static_cast<size_t>(t0 + t) * V + v);
+        add(c0, c1, x, t0, a.T - t0);
+      }
     }
   }
-  // 32 sums over 32 lanes: each step halves the values a lane still holds, and lane i ends with sum i
+  // 2 TC sums over 32 lanes: each step halves the values a lane still holds
+  int o = 16;
 #pragma unroll
-  for (int n = 16; n >= 1; n >>= 1) {
-    const bool up = lane & n;
+  for (int n = TC; n >= 1; n >>= 1, o >>= 1) {
+    const bool up = lane & o;
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       const double give = up ? acc[i] : acc[i + n];
       const double keep = up ? acc[i + n] : acc[i];
-      acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, n);
+      acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
     }
   }
-  sm->dots[warp][lane] = acc[0];
+#pragma unroll
+  for (; o >= 1; o >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
+  constexpr int SPREAD = 32 / (2 * TC);      // lanes that hold the same sum
+  if (lane % SPREAD == 0) sm->dots[warp][lane / SPREAD] = acc[0];
   named_bar_sync(1, CW * 32);
-  if (tid < 32) {
+  if (tid < 2 * TC) {
     double z = 0.0;
 #pragma unroll
     for (int w = 0; w < CW; ++w) z += sm->dots[w][tid];
-    const int t = tid & (MAX_T - 1), ex = tid < MAX_T ? e0 : e1;
+    const int t = tid % TC, ex = tid < TC ? e0 : e1;
     if (t < a.T && ex >= 0) {
       const float s = static_cast<float>(1.0 / (1.0 + exp(-z)));
       a.scores[t * a.N_r + ex] = make_float2(s + __ldg(a.b + ex), s);
@@ -388,14 +444,15 @@ __device__ __forceinline__ void unit_at(const Args& a, int unit, int& slot, int&
   ch = (unit - slot * per) * CH;
 }
 
-// The tokens' codes as operand tiles [d/128][rows8][128], 128-byte swizzle
+// The tokens' codes as operand tiles [d/128][R][128], 128-byte swizzle
 // (rows behind T stay unset), and their scales [d/128][16].
+template <int R>
 __device__ __forceinline__ void stage_tokens(const Args& a, uint8_t* xh, float* xs) {
   const int V = a.d >> 4, n = a.T * V;
 #pragma unroll 4
   for (int o = threadIdx.x; o < n; o += CW * 32) {
     const int t = o / V, v = o - t * V;
-    *reinterpret_cast<uint4*>(xh + (v >> 3) * (a.rows8 * 128) + t * 128 + (((v & 7) ^ (t & 7)) << 4)) =
+    *reinterpret_cast<uint4*>(xh + (v >> 3) * (R * 128) + t * 128 + (((v & 7) ^ (t & 7)) << 4)) =
         __ldcg(reinterpret_cast<const uint4*>(a.xq) + o);
   }
   const int kb_d = a.d >> 7;
@@ -407,25 +464,28 @@ __device__ __forceinline__ void stage_tokens(const Args& a, uint8_t* xh, float* 
 
 // ---------------------------------------------------------------- kernel
 
+template <int R>
 __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_constant__ Maps maps, const Args a) {
+  constexpr int EW = Shape<R>::EW, N = Shape<R>::N, BUF_COLS = Shape<R>::BUF_COLS, RED = Shape<R>::RED;
+  constexpr int tile_bytes = R * 128;                                // one block of the token operand
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem;
   uint8_t* xh = smem + static_cast<size_t>(a.stages) * STAGE;        // tokens' codes, then the H tiles
   float* xs = reinterpret_cast<float*>(xh + a.xh_bytes);             // [d/128][16]
-  float* red = xs + (a.d >> 7) * COLS;                               // [EW][gate, up][16][CH]
-  Small* sm = reinterpret_cast<Small*>(red + EW * RED);
+  float* red = xs + (a.d >> 7) * COLS;                               // [EW][PW][R][CH]
+  float* osum = red + EW * RED;                                      // [PW][R][32]
+  Small* sm = reinterpret_cast<Small*>(red + Shape<R>::FLOATS);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tile_bytes = a.rows8 * 128;                              // one block of the token operand
   const int kb_d = a.d >> 7, kb_i = a.I >> 7;
   volatile int* abort = &sm->abort;
 
   for (int i = threadIdx.x; i < MAX_N; i += THREADS) sm->mask[i] = 0u;
   if (threadIdx.x == 0) {
     for (int i = 0; i < MAX_STAGES; ++i) { mbar_init(&sm->full[i], 1); mbar_init(&sm->empty[i], 1); }
-    for (int i = 0; i < MAX_HBUF; ++i) { mbar_init(&sm->hfull[i], 1); mbar_init(&sm->hempty[i], 3); }
-    for (int i = 0; i < BUFS; ++i) { mbar_init(&sm->tfull[i], 1); mbar_init(&sm->tempty[i], 2); }
-    for (int i = 0; i < EW; ++i) { mbar_init(&sm->redfull[i], 2); mbar_init(&sm->redempty[i], 1); }
+    for (int i = 0; i < MAX_HBUF; ++i) { mbar_init(&sm->hfull[i], 1); mbar_init(&sm->hempty[i], 1 + PW); }
+    for (int i = 0; i < BUFS; ++i) { mbar_init(&sm->tfull[i], 1); mbar_init(&sm->tempty[i], PW); }
+    for (int i = 0; i < EW; ++i) { mbar_init(&sm->redfull[i], PW); mbar_init(&sm->redempty[i], 1); }
     mbar_init(&sm->sel_ready, 1);
     mbar_init(&sm->x_free, 1);
     mbar_init(&sm->drained, 1);
@@ -433,7 +493,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
     fence_mbar_init();
   }
   if (warp == CW + 1) {
-    tmem_alloc(&sm->tmem, TMEM_COLS);
+    tmem_alloc(&sm->tmem, Shape<R>::TMEM_COLS);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -492,186 +552,215 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
         mbar_wait(&sm->full[j % a.stages], (j / a.stages) & 1, abort);
     }
   } else if (warp == CW + 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = make_idesc(0, 0, 128, COLS);
-      bool ok = mbar_wait(&sm->sel_ready, 0, abort);
-      Cursor c, t;
-      t.lap = 1;
-      // one stage against nk blocks of the token operand at tok; the stage's blocks are `apart` bytes apart.
-      // MMAs into one sum wait for each other, so those of 2 QS sums are interleaved.
-      auto stage = [&](const uint8_t* tok, int nk, int apart) {
-        ok = ok && mbar_wait(&sm->tempty[t.i], t.lap, abort) && mbar_wait(&sm->full[c.i], c.lap, abort);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t ad = sw128_kmajor_desc(smem_u32(ring + c.i * STAGE));
-        const uint64_t bd = sw128_kmajor_desc(smem_u32(tok));
-        const uint32_t dt = tmem + t.i * BUF_COLS;
+    // ------------------------------------------------------------ MMA issuer (the whole warp keeps step)
+    if (lane > 0) {                             // the shared expert's gate and up codes on their way into L2
+      const size_t bytes = static_cast<size_t>(a.I) * a.d, piece = 4096;
+      const size_t first = bytes / piece * blockIdx.x / gridDim.x, last = bytes / piece * (blockIdx.x + 1) / gridDim.x;
+      for (size_t i = first + lane - 1; i < last; i += 31) {
+        prefetch_l2(a.w_gate_shared + i * piece, piece);
+        prefetch_l2(a.w_up_shared + i * piece, piece);
+      }
+    }
+    __syncwarp();
+    constexpr uint32_t idesc = make_idesc(0, 0, 128, N);
+    bool ok = warp_wait(&sm->sel_ready, 0, abort);
+    Cursor c, t;
+    t.lap = 1;
+    // one stage against the two blocks of the token operand at tok. MMAs into one sum wait for each other:
+    // QS sums are interleaved.
+    auto stage = [&](const uint8_t* tok) {
+      ok = ok && warp_wait(&sm->tempty[t.i], t.lap, abort) && warp_wait(&sm->full[c.i], c.lap, abort);
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t ad = sw128_kmajor_desc(smem_u32(ring + c.i * STAGE));
+      const uint64_t bd = sw128_kmajor_desc(smem_u32(tok));
+      const uint32_t dt = tmem + t.i * BUF_COLS;
+      if (lane == 0) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int j = 0; j < SK; ++j)
-            if (j < nk)
-              umma_f8f6f4(dt + (j * QS + q % QS) * COLS, ad + ((j * apart) >> 4) + 2 * q,
-                          bd + ((j * tile_bytes) >> 4) + 2 * q, idesc, q >= QS);
+        for (int q = 0; q < 4; ++q) umma_f8f6f4(dt + (q % QS) * N, ad + 2 * q, bd + 2 * q, idesc, q >= QS);
         umma_commit(&sm->empty[c.i]);
         umma_commit(&sm->tfull[t.i]);
-        c.next(a.stages);
-        t.next(BUFS);
-      };
-      if (ok) {
-        const int slots = sm->n_slots;
-        for (int unit = blockIdx.x; ok && unit < slots * per; unit += gridDim.x)
-          for (int k = 0; ok && k < kb_d; k += SK) stage(xh + k * tile_bytes, SK, STAGE / 4);
-        umma_commit(&sm->x_free);
-        Cursor h;
-        for (int si = 0; ok && si < slots; ++si) {
-          ok = mbar_wait(&sm->hfull[h.i], h.lap, abort);
-          const uint8_t* hb = xh + h.i * a.hbuf_bytes;
-          for (int k = 0; ok && k < kb_i; k += SK) stage(hb + k * tile_bytes, min(SK, kb_i - k), TILE);
-          umma_commit(&sm->hempty[h.i]);
-          h.next(a.hbufs);
-        }
       }
+      __syncwarp();
+      c.next(a.stages);
+      t.next(BUFS);
+    };
+    if (ok) {
+      const int slots = sm->n_slots;
+      for (int unit = blockIdx.x; ok && unit < slots * per; unit += gridDim.x)
+        for (int k = 0; ok && k < kb_d; k += SK) stage(xh + k * tile_bytes);
+      if (lane == 0) umma_commit(&sm->x_free);
+      Cursor h;
+      for (int si = 0; ok && si < slots; ++si) {
+        ok = warp_wait(&sm->hfull[h.i], h.lap, abort);
+        const uint8_t* hb = xh + h.i * a.hbuf_bytes;
+        for (int k = 0; ok && k < kb_i; k += SK) stage(hb + k * tile_bytes);
+        if (lane == 0) umma_commit(&sm->hempty[h.i]);
+        h.next(a.hbufs);
+      }
+    }
+    if (lane == 0) {
       umma_commit(&sm->drained);                // no MMA may run when the TMEM is freed
       mbar_wait(&sm->drained, 0, abort);
     }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ router and selection
     const int tid = threadIdx.x;
     if (a.xq_ws != nullptr) quantise_u(a);
-    for (int e0 = blockIdx.x; e0 < a.N_r; e0 += 2 * gridDim.x)
-      affinities(a, sm, e0, e0 + static_cast<int>(gridDim.x) < a.N_r ? e0 + static_cast<int>(gridDim.x) : -1);
+    for (int e0 = blockIdx.x; e0 < a.N_r; e0 += 2 * gridDim.x) {
+      const int e1 = e0 + static_cast<int>(gridDim.x) < a.N_r ? e0 + static_cast<int>(gridDim.x) : -1;
+      if (R == 8 && a.T <= LEAD) affinities<LEAD>(a, sm, e0, e1);
+      else affinities<R>(a, sm, e0, e1);
+    }
     __threadfence();
     named_bar_sync(1, CW * 32);
     if (tid == 0) count_up(a.grid_ctr);
-    if (a.xq_ws == nullptr) stage_tokens(a, xh, xs);          // given by the caller: no need to wait
+    if (a.xq_ws == nullptr) stage_tokens<R>(a, xh, xs);       // given by the caller: no need to wait
     if (tid == 0) count_wait(a.grid_ctr, gridDim.x, abort);
     named_bar_sync(1, CW * 32);
-    if (a.xq_ws != nullptr) stage_tokens(a, xh, xs);
+    if (a.xq_ws != nullptr) stage_tokens<R>(a, xh, xs);
     fence_proxy_async_smem();
     select_all(a, sm);
     if (tid == 0) mbar_arrive(&sm->sel_ready);
     const int slots = sm->n_slots, units = slots * per;
 
-    if (warp < 3) {
-      // ---------------------------------------------------------- sums of the partials: a thread owns a weight row
-      // first phase: gate rows are lanes 0..31 (warp 0), up rows lanes 64..95 (warp 2), the other lanes
-      // belong to the stage's other block; second phase: rows of W_down are lanes 0..63 (warps 0 and 1)
-      const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    if (warp < PW) {
+      // ---------------------------------------------------------- sums of the partials: a thread owns a TMEM lane
+      // first phase: lanes are 32 gate rows of block 0, of block 1, 32 up rows of block 0, of block 1;
+      // second phase: 64 rows of W_down in block 0, then in block 1
       bool ok = true;
       Cursor t, e;
       e.lap = 1;
-      float acc[COLS];
-      // the stage's partials, block j's in v[j * COLS ..]
-      auto partials = [&](float (&v)[SK * COLS]) {
+      // waits for the stage's partials; NC columns of this warp's quarter from column c0
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+      auto partials = [&](auto nc, int c0, float* v) {
+        constexpr int NC = decltype(nc)::value;
         ok = ok && warp_wait(&sm->tfull[t.i], t.lap, abort);
         if (ok) {
-          uint32_t lo[32], hi[32];
+          uint32_t r[QS * NC];
           tc_fence_after();
-          tmem_ld32_async(taddr + t.i * BUF_COLS, lo);
-          tmem_ld32_async(taddr + t.i * BUF_COLS + 32, hi);
-          tmem_wait_ld2(lo, hi);
+#pragma unroll
+          for (int q = 0; q < QS; ++q) tmem_ld_async<NC>(taddr + t.i * BUF_COLS + q * N + c0, r + q * NC);
+          tmem_wait_ld(r);
           tc_fence_before();
 #pragma unroll
-          for (int c = 0; c < COLS; ++c) {
-            v[c] = __uint_as_float(lo[c]) + __uint_as_float(lo[COLS + c]);
-            v[COLS + c] = __uint_as_float(hi[c]) + __uint_as_float(hi[COLS + c]);
-          }
+          for (int c = 0; c < NC; ++c) v[c] = __uint_as_float(r[c]) + __uint_as_float(r[NC + c]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->tempty[t.i]);
         t.next(BUFS);
       };
-      if (warp == 1) {
-        const int mine = units > static_cast<int>(blockIdx.x) ? (units - blockIdx.x - 1) / gridDim.x + 1 : 0;
-        const int passed = mine * (kb_d / SK);
-        t.i = passed % BUFS;
-        t.lap = (passed / BUFS) & 1;
-      } else {
-        for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+      {
+        const int half = warp & 1;
+        const float* s_all = warp < 2 ? a.s_gate : a.s_up;
+        // lane i: the weight scale of block 2 i + half of the unit at hand, loaded one unit ahead
+        auto scale_of = [&](int unit) {
           int slot, ch;
           unit_at(a, unit, slot, ch);
-          const float* sw = (warp == 0 ? a.s_gate : a.s_up) +
-                            (static_cast<size_t>(sm->slot_expert[slot]) * kb_i + (ch >> 7)) * kb_d;
+          const int kb = 2 * lane + half;
+          return kb < kb_d ? __ldg(s_all + (static_cast<size_t>(sm->slot_expert[slot]) * kb_i + (ch >> 7)) * kb_d + kb) : 0.0f;
+        };
+        float next = static_cast<int>(blockIdx.x) < units ? scale_of(blockIdx.x) : 0.0f;
+        for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+          const float mine = next;
+          if (unit + static_cast<int>(gridDim.x) < units) next = scale_of(unit + gridDim.x);
+          float acc[R];
 #pragma unroll
-          for (int c = 0; c < COLS; ++c) acc[c] = 0.0f;
+          for (int c = 0; c < R; ++c) acc[c] = 0.0f;
           for (int k = 0; k < kb_d; k += SK) {
-            float w[SK], v[SK * COLS];
-#pragma unroll
-            for (int j = 0; j < SK; ++j) w[j] = __ldg(sw + k + j);
-            partials(v);
+            float v[R];
+            partials(std::integral_constant<int, R>{}, half * R, v);
+            const float w = __shfl_sync(0xffffffffu, mine, k >> 1);
+            const float* x = xs + (k + half) * COLS;
             if (ok) {
 #pragma unroll
-              for (int j = 0; j < SK; ++j)
-#pragma unroll
-                for (int c = 0; c < COLS; c += 4) {
-                  const float4 x = *reinterpret_cast<const float4*>(xs + (k + j) * COLS + c);
-                  acc[c] = fmaf(v[j * COLS + c], x.x * w[j], acc[c]);
-                  acc[c + 1] = fmaf(v[j * COLS + c + 1], x.y * w[j], acc[c + 1]);
-                  acc[c + 2] = fmaf(v[j * COLS + c + 2], x.z * w[j], acc[c + 2]);
-                  acc[c + 3] = fmaf(v[j * COLS + c + 3], x.w * w[j], acc[c + 3]);
-                }
+              for (int c = 0; c < R; c += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(x + c);
+                acc[c] = fmaf(v[c], f.x * w, acc[c]);
+                acc[c + 1] = fmaf(v[c + 1], f.y * w, acc[c + 1]);
+                acc[c + 2] = fmaf(v[c + 2], f.z * w, acc[c + 2]);
+                acc[c + 3] = fmaf(v[c + 3], f.w * w, acc[c + 3]);
+              }
             }
           }
           ok = ok && warp_wait(&sm->redempty[e.i], e.lap, abort);
           if (ok) {
-            float* p = red + e.i * RED + (warp >> 1) * COLS * CH + lane;
+            float* p = red + e.i * RED + warp * R * CH + lane;
 #pragma unroll
-            for (int c = 0; c < COLS; ++c) p[c * CH] = acc[c];
+            for (int c = 0; c < R; ++c) p[c * CH] = acc[c];
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm->redfull[e.i]);
           e.next(EW);
         }
       }
-      if (warp < 2) {
-        // W_down: the CTA's rows over every slot
+
+      // W_down: the CTA's rows over every slot, whose tokens are the first columns
+      const int half = warp >> 1;
+      const int r = (warp & 1) * 32 + lane;
+      const int nb0 = row0 >> 7;                // rows of one or two 128-row blocks
+      const bool upper = ((row0 + min(r, max(nrows - 1, 0))) >> 7) != nb0;
+      float* sums = osum + warp * R * 32 + lane;
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) acc[c] = 0.0f;
-        const int r = warp * 32 + lane;
-        const int nb = (row0 + min(r, max(nrows - 1, 0))) >> 7;
-        Cursor h;
-        for (int si = 0; si < slots; ++si) {
-          const int ex = sm->slot_expert[si];
-          const uint32_t mask = si == 0 ? (1u << a.T) - 1u : sm->mask[ex];
-          const float* sw = a.s_down + (static_cast<size_t>(ex) * kb_d + nb) * kb_i;
-          ok = ok && warp_wait(&sm->hfull[h.i], h.lap, abort);
-          const float* hs = reinterpret_cast<const float*>(xh + h.i * a.hbuf_bytes + kb_i * tile_bytes);
+      for (int c = 0; c < R; ++c) sums[c * 32] = 0.0f;
+      auto scales_of = [&](int si, float& lo, float& hi) {
+        const float* sw = a.s_down + (static_cast<size_t>(sm->slot_expert[si]) * kb_d + nb0) * kb_i;
+        const int kb = 2 * lane + half;
+        lo = hi = 0.0f;
+        if (kb < kb_i) {
+          lo = __ldg(sw + kb);
+          if (nb0 + 1 < kb_d) hi = __ldg(sw + kb_i + kb);
+        }
+      };
+      Cursor h;
+      float next_lo, next_hi;
+      scales_of(0, next_lo, next_hi);
+      for (int si = 0; si < slots; ++si) {
+        const float lo = next_lo, hi = next_hi;
+        if (si + 1 < slots) scales_of(si + 1, next_lo, next_hi);
+        ok = ok && warp_wait(&sm->hfull[h.i], h.lap, abort);
+        const float* hs = reinterpret_cast<const float*>(xh + h.i * a.hbuf_bytes + kb_i * tile_bytes);
+        const int first = sm->slot_start[si], ntok = sm->slot_start[si + 1] - first;
+        auto rows = [&](auto nc) {
+          constexpr int NC = decltype(nc)::value;
+          float acc[NC];
+#pragma unroll
+          for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
           for (int k = 0; k < kb_i; k += SK) {
-            const int nk = min(SK, kb_i - k);
-            float w[SK], v[SK * COLS];
+            float v[NC];
+            partials(nc, half * R, v);
+            const float wl = __shfl_sync(0xffffffffu, lo, k >> 1), wh = __shfl_sync(0xffffffffu, hi, k >> 1);
+            const float w = upper ? wh : wl;
+            if (ok && k + half < kb_i) {
 #pragma unroll
-            for (int j = 0; j < SK; ++j) w[j] = j < nk ? __ldg(sw + k + j) : 0.0f;
-            partials(v);
-            if (ok) {
-#pragma unroll
-              for (int j = 0; j < SK; ++j)
-                if (j < nk) {
-#pragma unroll
-                  for (int c = 0; c < COLS; ++c)
-                    if ((mask >> c) & 1u)          // others hold no token of this slot, and anything
-                      acc[c] = fmaf(v[j * COLS + c], hs[(k + j) * COLS + c] * w[j], acc[c]);
-                }
+              for (int c = 0; c < NC; ++c) acc[c] = fmaf(v[c], hs[(k + half) * COLS + c] * w, acc[c]);
             }
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm->hempty[h.i]);
-          h.next(a.hbufs);
-        }
-        const uint16_t* base = a.base != nullptr ? a.base : a.u;
-        if (r < nrows) {
 #pragma unroll
-          for (int c = 0; c < COLS; ++c)
-            if (c < a.T) {
-              const size_t at = static_cast<size_t>(c) * a.d + row0 + r;
-              a.out[at] = float_to_bf16_bits(bf16_bits_to_float(base[at]) + acc[c]);
-            }
-        }
+          for (int c = 0; c < NC; ++c)
+            if (c < ntok) sums[sm->ent_tok[first + c] * 32] += acc[c];
+        };
+        if (ntok <= 2) rows(std::integral_constant<int, 2>{});
+        else if (ntok <= 4) rows(std::integral_constant<int, 4>{});
+        else if (R == 8 || ntok <= 8) rows(std::integral_constant<int, 8>{});
+        else rows(std::integral_constant<int, R>{});
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->hempty[h.i]);
+        h.next(a.hbufs);
       }
-    } else if (warp < 3 + EW) {
+      // both blocks' sums, and the outputs
+      named_bar_sync(3, PW * 32);
+      const uint16_t* base = a.base != nullptr ? a.base : a.u;
+      if (r < nrows)
+        for (int c = half; c < a.T; c += 2) {
+          const size_t at = static_cast<size_t>(c) * a.d + row0 + r;
+          const float* p = osum + ((warp & 1) * R + c) * 32 + lane;
+          a.out[at] = float_to_bf16_bits(bf16_bits_to_float(base[at]) + (p[0] + p[2 * R * 32]));
+        }
+    } else if (warp < PW + EW) {
       // ---------------------------------------------------------- finishing warps: SwiGLU, then the blocks' codes
-      const int e = warp - 3;
+      const int e = warp - PW;
       uint32_t lap = 0;
       for (int unit = blockIdx.x + e * gridDim.x; unit < units; unit += EW * gridDim.x, lap ^= 1) {
         if (!warp_wait(&sm->redfull[e], lap, abort)) break;
@@ -681,7 +770,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
         const float* p = red + e * RED + lane;
         for (int j = 0; j < ntok; ++j) {
           const int t = sm->ent_tok[first + j];
-          const float g = p[t * CH], u = p[(COLS + t) * CH];
+          const float g = p[t * CH] + p[(R + t) * CH], u = p[(2 * R + t) * CH] + p[(3 * R + t) * CH];
           a.act[static_cast<size_t>(sm->ent_row[first + j]) * a.I + ch + lane] = __fdiv_rn(g, 1.0f + expf(-g)) * u;
         }
         __syncwarp();
@@ -695,13 +784,13 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
         if (__shfl_sync(0xffffffffu, last, 0)) {
           __threadfence();
           for (int j = 0; j < ntok; ++j) {
-            const int r = sm->ent_row[first + j], t = sm->ent_tok[first + j];
+            const int r = sm->ent_row[first + j];
             const float4 x = __ldcg(reinterpret_cast<const float4*>(a.act + static_cast<size_t>(r) * a.I + blk * 128) + lane);
             float amax = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
             const float s = tile_scale(amax);
-            reinterpret_cast<uint32_t*>(a.hq + static_cast<size_t>(r) * a.I + blk * 128)[lane ^ ((t & 7) << 2)] =
+            reinterpret_cast<uint32_t*>(a.hq + static_cast<size_t>(r) * a.I + blk * 128)[lane ^ ((j & 7) << 2)] =
                 e4m3x2(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s)) | (e4m3x2(__fdiv_rn(x.z, s), __fdiv_rn(x.w, s)) << 16);
             if (lane == 0) a.hs[r * kb_i + blk] = s;
           }
@@ -711,7 +800,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
           if (lane == 0) count_up(a.slot_done + slot);
         }
       }
-    } else if (warp == 3 + EW) {
+    } else if (warp == PW + EW) {
       // ---------------------------------------------------------- loader of the H tiles, over the tokens' operand
       bool ok = warp_wait(&sm->x_free, 0, abort);
       Cursor h;
@@ -728,14 +817,14 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
         float* hs = reinterpret_cast<float*>(hb + kb_i * tile_bytes);
         for (int o = lane; o < ntok * kb_i; o += 32) {
           const int j = o / kb_i, k = o - j * kb_i;
-          hs[k * COLS + sm->ent_tok[first + j]] = __ldcg(a.hs + sm->ent_row[first + j] * kb_i + k) * sm->ent_gate[first + j];
+          hs[k * COLS + j] = __ldcg(a.hs + sm->ent_row[first + j] * kb_i + k) * sm->ent_gate[first + j];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&sm->hfull[h.i], ntok * a.I);
         __syncwarp();
         for (int o = lane; o < ntok * kb_i; o += 32) {
           const int j = o / kb_i, k = o - j * kb_i;
-          bulk_load(hb + k * tile_bytes + sm->ent_tok[first + j] * 128,
+          bulk_load(hb + k * tile_bytes + j * 128,
                     a.hq + static_cast<size_t>(sm->ent_row[first + j]) * a.I + k * 128, 128, &sm->hfull[h.i]);
         }
         h.next(a.hbufs);
@@ -747,7 +836,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
   __syncthreads();
   if (warp == CW + 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, TMEM_COLS);
+    tmem_dealloc(tmem, Shape<R>::TMEM_COLS);
   }
 }
 
@@ -785,6 +874,37 @@ inline int make_map(CUtensorMap* m, const void* base, size_t rows, int cols) {
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? MOE_OK : record_failure(MOE_ERR_CUDA, "cuTensorMapEncodeTiled", "few tokens: weight map");
+}
+
+template <int R>
+int launch(const Maps& maps, Args& a, int G, cudaStream_t s) {
+  // shared memory: the token operand and the H tiles take turns in one
+  // region; the ring gets what is left
+  const int x_bytes = (a.d / 128) * R * 128;
+  a.hbuf_bytes = static_cast<int>(round_up((a.I / 128) * (R * 128 + COLS * 4), 1024));
+  a.xh_bytes = x_bytes > a.hbuf_bytes ? x_bytes : a.hbuf_bytes;
+  if (a.xh_bytes < 2 * a.hbuf_bytes && 2 * a.hbuf_bytes <= 96 * 1024) a.xh_bytes = 2 * a.hbuf_bytes;
+  a.hbufs = a.xh_bytes / a.hbuf_bytes;
+  if (a.hbufs > MAX_HBUF) a.hbufs = MAX_HBUF;
+  const size_t rest = a.xh_bytes + (a.d / 128) * COLS * 4 + Shape<R>::FLOATS * 4 + sizeof(Small);
+  a.stages = static_cast<int>((SMEM_MAX - rest) / STAGE);
+  if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
+  const size_t smem = rest + static_cast<size_t>(a.stages) * STAGE;
+  auto k = few_tokens_kernel<R>;
+  if (int st = cuda_status(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)),
+                           "few tokens: smem attribute"))
+    return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(G);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeCooperative;       // the CTAs wait for one another
+  at[0].val.cooperative = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, k, maps, static_cast<const Args>(a)), "few tokens: launch");
 }
 
 inline bool sizes_supported(int T, int d, int N_r, int K_r, int I) {
@@ -844,19 +964,8 @@ extern "C" int moe_few_tokens(const uint16_t* u, const uint8_t* xq, const float*
   a.hs = reinterpret_cast<float*>(ws + l.hs);
   a.T = T; a.d = d; a.N_r = N_r; a.K = K_r; a.I = I;
 
-  // shared memory: the token operand (8 or 16 rows a block) and the H tiles
-  // take turns in one region; the ring gets what is left
-  a.rows8 = T <= 8 ? 8 : 16;
-  const int x_bytes = (d / 128) * a.rows8 * 128;
-  a.hbuf_bytes = static_cast<int>(round_up((I / 128) * (a.rows8 * 128 + COLS * 4), 1024));
-  a.xh_bytes = x_bytes > a.hbuf_bytes ? x_bytes : a.hbuf_bytes;
-  if (a.xh_bytes < 2 * a.hbuf_bytes && 2 * a.hbuf_bytes <= 96 * 1024) a.xh_bytes = 2 * a.hbuf_bytes;
-  a.hbufs = a.xh_bytes / a.hbuf_bytes;
-  if (a.hbufs > MAX_HBUF) a.hbufs = MAX_HBUF;
-  const size_t rest = a.xh_bytes + (d / 128) * COLS * 4 + EW * RED * 4 + sizeof(Small);
-  a.stages = static_cast<int>((SMEM_MAX - rest) / STAGE);
-  if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
-  const size_t smem = rest + static_cast<size_t>(a.stages) * STAGE;
+  a.w_gate_shared = w_gate + static_cast<size_t>(N_r) * I * d;
+  a.w_up_shared = w_up + static_cast<size_t>(N_r) * I * d;
 
   Maps maps;
   const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -868,19 +977,5 @@ extern "C" int moe_few_tokens(const uint16_t* u, const uint8_t* xq, const float*
     if (int st = make_tmap_2d(&maps.down[i], w_down, U8, 1, slots * d, I, n > 0 ? n : 1, 128)) return st;
   }
   if (int st = cuda_status(cudaMemsetAsync(ws, 0, l.ctr_bytes, s), "few tokens: counters")) return st;
-  if (int st = cuda_status(cudaFuncSetAttribute(few_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                static_cast<int>(smem)),
-                           "few tokens: smem attribute"))
-    return st;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(G);
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeCooperative;       // every CTA waits for every other twice
-  at[0].val.cooperative = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, few_tokens_kernel, maps, static_cast<const Args>(a)), "few tokens: launch");
+  return T <= 8 ? launch<8>(maps, a, G, s) : launch<16>(maps, a, G, s);
 }
