@@ -32,8 +32,10 @@ constexpr int MAX_SLOTS = MAX_N + 1;
 constexpr int MAX_ENTRIES = MAX_T * MAX_K + MAX_T;
 constexpr int MAX_D = 8192;
 constexpr int CW = 8;                        // warps of the router and the selection
+constexpr int EW_MAX = 3;                    // of them, finishing warps of the first phase
 constexpr int PW = 4;                        // of them, warps that add up partials, one per 32 TMEM lanes
-constexpr int THREADS = (CW + 2) * 32;       // and the producer, the MMA issuer
+constexpr int MI = 2;                        // MMA issuers, which take turns (stages and TMEM buffers are multiples of it)
+constexpr int THREADS = (CW + 1 + MI) * 32;  // and the producer
 constexpr int CH = 32;                       // intermediate channels of a unit
 constexpr int LIVE = 64;                     // live weight rows of a tile
 constexpr int SK = 2;                        // 128-channel blocks of a stage
@@ -75,18 +77,16 @@ struct Args {
   uint8_t* hq;              // [T*K + T][I] its codes, 16-byte words swizzled by place in the slot
   float* hs;                // [T*K + T][I/128]
   int T, d, N_r, K, I;
-  int stages, hbufs, xh_bytes, hbuf_bytes;
+  int stages, hbufs, xh_bytes, hbuf_bytes, ew;   // ew: finishing warps, a buffer of sums each
 };
 
 // R: token rows of an operand tile (T rounded up to 8).
 template <int R>
 struct Shape {
-  static constexpr int EW = R == 8 ? 3 : 2;                 // finishing warps of the first phase
   static constexpr int N = SK * R;                          // MMA columns: token rows of the stage's two blocks
   static constexpr int BUF_COLS = QS * N;                   // TMEM columns of a stage's partials
   static constexpr int TMEM_COLS = BUFS * BUF_COLS;
-  static constexpr int RED = PW * R * CH;                   // floats of one unit's sums
-  static constexpr int FLOATS = EW * RED + PW * R * 32;     // with the outputs' sums
+  static constexpr int RED = PW * R * CH;                   // floats of one unit's sums, and of the outputs' sums
 };
 
 // Shared memory behind the dynamic regions.
@@ -94,7 +94,7 @@ struct Small {
   uint64_t full[MAX_STAGES], empty[MAX_STAGES];
   uint64_t hfull[MAX_HBUF], hempty[MAX_HBUF];
   uint64_t tfull[BUFS], tempty[BUFS];
-  uint64_t redfull[3], redempty[3];
+  uint64_t redfull[EW_MAX], redempty[EW_MAX];
   uint64_t sel_ready, x_free, drained;
   uint32_t tmem;
   int abort;
@@ -466,15 +466,15 @@ __device__ __forceinline__ void stage_tokens(const Args& a, uint8_t* xh, float* 
 
 template <int R>
 __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_constant__ Maps maps, const Args a) {
-  constexpr int EW = Shape<R>::EW, N = Shape<R>::N, BUF_COLS = Shape<R>::BUF_COLS, RED = Shape<R>::RED;
+  constexpr int N = Shape<R>::N, BUF_COLS = Shape<R>::BUF_COLS, RED = Shape<R>::RED;
   constexpr int tile_bytes = R * 128;                                // one block of the token operand
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem;
   uint8_t* xh = smem + static_cast<size_t>(a.stages) * STAGE;        // tokens' codes, then the H tiles
   float* xs = reinterpret_cast<float*>(xh + a.xh_bytes);             // [d/128][16]
-  float* red = xs + (a.d >> 7) * COLS;                               // [EW][PW][R][CH]
-  float* osum = red + EW * RED;                                      // [PW][R][32]
-  Small* sm = reinterpret_cast<Small*>(red + Shape<R>::FLOATS);
+  float* red = xs + (a.d >> 7) * COLS;                               // [ew][PW][R][CH]
+  float* osum = reinterpret_cast<float*>(xh + a.hbufs * a.hbuf_bytes);   // [PW][R][32], in the second phase
+  Small* sm = reinterpret_cast<Small*>(red + a.ew * RED);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kb_d = a.d >> 7, kb_i = a.I >> 7;
@@ -483,12 +483,12 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
   for (int i = threadIdx.x; i < MAX_N; i += THREADS) sm->mask[i] = 0u;
   if (threadIdx.x == 0) {
     for (int i = 0; i < MAX_STAGES; ++i) { mbar_init(&sm->full[i], 1); mbar_init(&sm->empty[i], 1); }
-    for (int i = 0; i < MAX_HBUF; ++i) { mbar_init(&sm->hfull[i], 1); mbar_init(&sm->hempty[i], 1 + PW); }
+    for (int i = 0; i < MAX_HBUF; ++i) { mbar_init(&sm->hfull[i], 1); mbar_init(&sm->hempty[i], MI + PW); }
     for (int i = 0; i < BUFS; ++i) { mbar_init(&sm->tfull[i], 1); mbar_init(&sm->tempty[i], PW); }
-    for (int i = 0; i < EW; ++i) { mbar_init(&sm->redfull[i], PW); mbar_init(&sm->redempty[i], 1); }
+    for (int i = 0; i < EW_MAX; ++i) { mbar_init(&sm->redfull[i], PW); mbar_init(&sm->redempty[i], 1); }
     mbar_init(&sm->sel_ready, 1);
-    mbar_init(&sm->x_free, 1);
-    mbar_init(&sm->drained, 1);
+    mbar_init(&sm->x_free, MI);
+    mbar_init(&sm->drained, MI);
     sm->abort = 0;
     fence_mbar_init();
   }
@@ -551,9 +551,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
       for (int j = max(0, issued - a.stages); j < issued; ++j)
         mbar_wait(&sm->full[j % a.stages], (j / a.stages) & 1, abort);
     }
-  } else if (warp == CW + 1) {
-    // ------------------------------------------------------------ MMA issuer (the whole warp keeps step)
-    if (lane > 0) {                             // the shared expert's gate and up codes on their way into L2
+  } else if (warp > CW) {
+    // ------------------------------------------------------------ MMA issuers (the whole warp keeps step)
+    if (warp == CW + 1 && lane > 0) {                             // the shared expert's gate and up codes on their way into L2
       const size_t bytes = static_cast<size_t>(a.I) * a.d, piece = 4096;
       const size_t first = bytes / piece * blockIdx.x / gridDim.x, last = bytes / piece * (blockIdx.x + 1) / gridDim.x;
       for (size_t i = first + lane - 1; i < last; i += 31) {
@@ -566,9 +566,16 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
     bool ok = warp_wait(&sm->sel_ready, 0, abort);
     Cursor c, t;
     t.lap = 1;
+    int turn = warp - CW - 1;                   // stages until this warp's next one
     // one stage against the two blocks of the token operand at tok. MMAs into one sum wait for each other:
     // QS sums are interleaved.
     auto stage = [&](const uint8_t* tok) {
+      if (turn-- > 0) {
+        c.next(a.stages);
+        t.next(BUFS);
+        return;
+      }
+      turn = MI - 1;
       ok = ok && warp_wait(&sm->tempty[t.i], t.lap, abort) && warp_wait(&sm->full[c.i], c.lap, abort);
       if (!ok) return;
       tc_fence_after();
@@ -692,7 +699,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm->redfull[e.i]);
-          e.next(EW);
+          e.next(a.ew);
         }
       }
 
@@ -758,11 +765,11 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
           const float* p = osum + ((warp & 1) * R + c) * 32 + lane;
           a.out[at] = float_to_bf16_bits(bf16_bits_to_float(base[at]) + (p[0] + p[2 * R * 32]));
         }
-    } else if (warp < PW + EW) {
+    } else if (warp < PW + EW_MAX) {
       // ---------------------------------------------------------- finishing warps: SwiGLU, then the blocks' codes
       const int e = warp - PW;
       uint32_t lap = 0;
-      for (int unit = blockIdx.x + e * gridDim.x; unit < units; unit += EW * gridDim.x, lap ^= 1) {
+      for (int unit = blockIdx.x + e * gridDim.x; e < a.ew && unit < units; unit += a.ew * gridDim.x, lap ^= 1) {
         if (!warp_wait(&sm->redfull[e], lap, abort)) break;
         int slot, ch;
         unit_at(a, unit, slot, ch);
@@ -800,7 +807,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
           if (lane == 0) count_up(a.slot_done + slot);
         }
       }
-    } else if (warp == PW + EW) {
+    } else if (warp == PW + EW_MAX) {
       // ---------------------------------------------------------- loader of the H tiles, over the tokens' operand
       bool ok = warp_wait(&sm->x_free, 0, abort);
       Cursor h;
@@ -881,14 +888,20 @@ int launch(const Maps& maps, Args& a, int G, cudaStream_t s) {
   // shared memory: the token operand and the H tiles take turns in one
   // region; the ring gets what is left
   const int x_bytes = (a.d / 128) * R * 128;
+  const int osum = Shape<R>::RED * 4;            // the outputs' sums, behind the H tiles
   a.hbuf_bytes = static_cast<int>(round_up((a.I / 128) * (R * 128 + COLS * 4), 1024));
-  a.xh_bytes = x_bytes > a.hbuf_bytes ? x_bytes : a.hbuf_bytes;
-  if (a.xh_bytes < 2 * a.hbuf_bytes && 2 * a.hbuf_bytes <= 96 * 1024) a.xh_bytes = 2 * a.hbuf_bytes;
-  a.hbufs = a.xh_bytes / a.hbuf_bytes;
+  const int h_bytes = (2 * a.hbuf_bytes <= 96 * 1024 ? 2 : 1) * a.hbuf_bytes + osum;
+  a.xh_bytes = x_bytes > h_bytes ? x_bytes : h_bytes;
+  a.hbufs = (a.xh_bytes - osum) / a.hbuf_bytes;
   if (a.hbufs > MAX_HBUF) a.hbufs = MAX_HBUF;
-  const size_t rest = a.xh_bytes + (a.d / 128) * COLS * 4 + Shape<R>::FLOATS * 4 + sizeof(Small);
+  // short units (small d) need several finishing warps; with long ones one keeps up, and its buffer's
+  // room goes to the ring
+  a.ew = R == 16 && a.d > 4096 ? 1 : EW_MAX;
+  const size_t rest = a.xh_bytes + (a.d / 128) * COLS * 4 + a.ew * Shape<R>::RED * 4 + sizeof(Small);
   a.stages = static_cast<int>((SMEM_MAX - rest) / STAGE);
   if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
+  a.stages -= a.stages % MI;                     // an issuer owns its stages: it never waits for another's lap
+  static_assert(MAX_STAGES % MI == 0 && BUFS % MI == 0, "stages and buffers are dealt to the issuers");
   const size_t smem = rest + static_cast<size_t>(a.stages) * STAGE;
   auto k = few_tokens_kernel<R>;
   if (int st = cuda_status(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)),
