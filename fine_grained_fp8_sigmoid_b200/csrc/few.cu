@@ -1,13 +1,14 @@
-// The whole layer for at most 16 tokens in one kernel: router, selection,
-// selected experts and the shared one, combine.
+// The whole layer for at most 16 tokens in two kernels: the router's affinities
+// (and u's quantisation), then selection, selected experts and the shared one,
+// combine.
 //
 // Every byte of the touched experts' weights is read once and nothing else is
-// large, so the kernel is a stream of weights: one CTA per SM (a cooperative
-// launch), a producer that keeps a ring of TMA boxes in flight across all
-// phases, and the tensor cores behind it. The weights do not depend on what the
-// phases exchange, only on the selection, so the ring fills with the shared
-// expert while the router runs and with W_down while the last intermediate rows
-// are written.
+// large, so the second kernel is a stream of weights: one CTA per SM (a
+// cooperative launch), a producer that keeps a ring of TMA boxes in flight
+// across its phases, and the tensor cores behind it. The weights do not depend
+// on what the phases exchange, only on the selection, so the ring fills with
+// the shared expert during the selection and with W_down while the last
+// intermediate rows are written.
 //
 // Products: weight rows are the MMA's M side, tokens its N side. A stage of the
 // ring holds two 128-channel blocks of 64 weight rows, and one MMA takes both:
@@ -31,7 +32,7 @@ constexpr int MAX_N = 256;
 constexpr int MAX_SLOTS = MAX_N + 1;
 constexpr int MAX_ENTRIES = MAX_T * MAX_K + MAX_T;
 constexpr int MAX_D = 8192;
-constexpr int CW = 8;                        // warps of the router and the selection
+constexpr int CW = 8;                        // warps of the selection
 constexpr int EW_MAX = 3;                    // of them, finishing warps of the first phase
 constexpr int PW = 4;                        // of them, warps that add up partials, one per 32 TMEM lanes
 constexpr int MI = 2;                        // MMA issuers, which take turns (stages and TMEM buffers are multiples of it)
@@ -63,24 +64,28 @@ struct Args {
   const float* xs;
   uint8_t* xq_ws;           // not NULL: quantise u into the workspace
   float* xs_ws;
-  const uint8_t *w_gate_shared, *w_up_shared;
   const float *s_gate, *s_up, *s_down;
   uint16_t* out;
   int32_t* topk_idx;
   float* gates;
   int32_t* counts;
-  unsigned* grid_ctr;       // CTAs whose affinities are written
   unsigned* slot_done;      // [slot] quantised blocks of its H
   int* blk_ctr;             // [slot][I/128]: finished units of a block
   float2* scores;           // [T][N_r] key s + b, affinity s
   float* act;               // [T*K + T][I] silu(G) U
   uint8_t* hq;              // [T*K + T][I] its codes, 16-byte words swizzled by place in the slot
-  float* hs;                // [T*K + T][I/128]
+  float* hs;                // [T*K + T][hs_pitch] its I/128 scales
   int T, d, N_r, K, I;
+  int sk2;                  // blocks of a second-phase stage: SK, or 2 SK where a CTA has at most 32 rows
+  int ctr_words;            // slot_done and blk_ctr, zeroed by the first kernel
+  int hs_pitch;             // I/128 rounded up to 4
   int stages, hbufs, xh_bytes, hbuf_bytes, ew;   // ew: finishing warps, a buffer of sums each
 };
 
 // R: token rows of an operand tile (T rounded up to 8).
+template <int N>
+using Int = std::integral_constant<int, N>;
+
 template <int R>
 struct Shape {
   static constexpr int N = SK * R;                          // MMA columns: token rows of the stage's two blocks
@@ -95,7 +100,7 @@ struct Small {
   uint64_t hfull[MAX_HBUF], hempty[MAX_HBUF];
   uint64_t tfull[BUFS], tempty[BUFS];
   uint64_t redfull[EW_MAX], redempty[EW_MAX];
-  uint64_t sel_ready, x_free, drained;
+  uint64_t sel_ready, x_ready, x_free, drained;
   uint32_t tmem;
   int abort;
   int n_slots;
@@ -107,7 +112,6 @@ struct Small {
   uint8_t ent_tok[MAX_ENTRIES];
   float ent_gate[MAX_ENTRIES];
   int chunk_slots[CW], chunk_ents[CW];
-  double dots[CW][32];
 };
 
 // A position in a ring of barriers: index and the parity of its lap.
@@ -138,10 +142,6 @@ __device__ __forceinline__ void box_load(void* dst, const CUtensorMap* m, uint64
       : "memory");
 }
 
-__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
 // Issues a read of NC consecutive FP32 columns of the thread's TMEM lane.
 template <int NC>
 __device__ __forceinline__ void tmem_ld_async(uint32_t taddr, uint32_t* r) {
@@ -165,13 +165,17 @@ __device__ __forceinline__ void count_up(unsigned* ctr) {
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(ctr) : "memory");
 }
 
+__device__ __forceinline__ unsigned count_now(const unsigned* ctr) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(ctr) : "memory");
+  return v;
+}
+
 // Waits until a counter has reached n; bounded as mbar_wait is.
 __device__ __forceinline__ bool count_wait(const unsigned* ctr, unsigned n, volatile int* abort) {
   uint64_t t0 = 0;
   for (uint32_t i = 0;; ++i) {
-    unsigned v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(ctr) : "memory");
-    if (v >= n) return true;
+    if (count_now(ctr) >= n) return true;
     if ((i & 63) == 63) {
       if (*abort) return false;
       const uint64_t t = globaltimer_ns();
@@ -191,11 +195,10 @@ __host__ __device__ inline int range_begin(int i, int n, int parts) {
 
 // ---------------------------------------------------------------- router
 
-// Affinities of experts e0 and e1 (e1 < 0: none) with every token. The
-// selection is a border, so the logits are summed in FP64 (their products are
-// exact) and the affinity is rounded once: keys that differ in FP32 are never
-// exchanged by the sum's order. FP64 costs conversions and DFMAs, which run
-// while the ring fills.
+// Affinities of EB experts with TB tokens, a block of 8 warps. The selection is
+// a border, so the logits are summed in FP64 (their products are exact) and the
+// affinity is rounded once: keys that differ in FP32 are never exchanged by the
+// sum's order. EB x TB keeps what the blocks read from L2 together small.
 __device__ __forceinline__ void to_double8(const uint4 v, double (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -205,66 +208,55 @@ __device__ __forceinline__ void to_double8(const uint4 v, double (&f)[8]) {
   }
 }
 
-// TC: token capacity. Up to LEAD tokens load everything ahead (one latency).
-constexpr int LEAD = 4;
-template <int TC>
-__device__ __forceinline__ void affinities(const Args& a, Small* sm, int e0, int e1) {
+__device__ __forceinline__ void quantise_u(const Args& a, int block, int blocks);
+
+template <int EB, int TB>
+__global__ void __launch_bounds__(256) few_route_kernel(const Args a) {
+  constexpr int M = EB * TB;                 // sums of a thread: 8 or 32
+  static_assert(M <= 32 && (M & (M - 1)) == 0, "the sums spread over a warp's lanes");
+  __shared__ double dots[8][M];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  double acc[2 * TC];                        // [expert][token]
-#pragma unroll
-  for (int i = 0; i < 2 * TC; ++i) acc[i] = 0.0;
+  const int block = blockIdx.y * gridDim.x + blockIdx.x, blocks = gridDim.x * gridDim.y;
+  const int e0 = blockIdx.x * EB, t0 = blockIdx.y * TB;
   const int V = a.d >> 3;                    // at most four runs of 8 channels a thread
-  const uint4* r0 = reinterpret_cast<const uint4*>(a.e + static_cast<size_t>(e0) * a.d);
-  const uint4* r1 = reinterpret_cast<const uint4*>(a.e + static_cast<size_t>(e1 < 0 ? e0 : e1) * a.d);
-  const uint4* ru = reinterpret_cast<const uint4*>(a.u);
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  auto add = [&](const uint4 n0, const uint4 n1, const uint4* x, int t0, int n) {
-    double w0[8], w1[8], f[8];
-    to_double8(n0, w0);
-    to_double8(n1, w1);
+  double acc[M];
 #pragma unroll
-    for (int t = 0; t < (TC < 8 ? TC : 8); ++t)
-      if (t < n) {
-        to_double8(x[t], f);
+  for (int i = 0; i < M; ++i) acc[i] = 0.0;
+  constexpr int AHEAD = M <= 8 ? 4 : 1;      // few sums leave registers to load all four runs at once
+#pragma unroll 1
+  for (int r = 0; r < 4; r += AHEAD) {
+    uint4 we[AHEAD][EB], x[AHEAD][TB];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          acc[t0 + t] = fma(f[j], w0[j], acc[t0 + t]);
-          acc[TC + t0 + t] = fma(f[j], w1[j], acc[TC + t0 + t]);
-        }
-      }
-  };
-  if constexpr (TC <= LEAD) {
-    uint4 we[4][2], x[4][TC];
+    for (int i = 0; i < AHEAD; ++i) {
+      const int v = tid + (r + i) * 256;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int v = tid + i * CW * 32;
-      we[i][0] = v < V ? __ldg(r0 + v) : zero;
-      we[i][1] = v < V ? __ldg(r1 + v) : zero;
+      for (int k = 0; k < EB; ++k)
+        we[i][k] = v < V && e0 + k < a.N_r ? __ldg(reinterpret_cast<const uint4*>(a.e + static_cast<size_t>(e0 + k) * a.d) + v) : zero;
 #pragma unroll
-      for (int t = 0; t < TC; ++t) x[i][t] = v < V && t < a.T ? __ldg(ru + static_cast<size_t>(t) * V + v) : zero;
+      for (int t = 0; t < TB; ++t)
+        x[i][t] = v < V && t0 + t < a.T ? __ldg(reinterpret_cast<const uint4*>(a.u + static_cast<size_t>(t0 + t) * a.d) + v) : zero;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) add(we[i][0], we[i][1], x[i], 0, a.T);
-  } else {
-    int v = tid;
-    uint4 n0 = v < V ? __ldg(r0 + v) : zero, n1 = v < V ? __ldg(r1 + v) : zero;
-    for (; v < V; v += CW * 32) {
-      const uint4 c0 = n0, c1 = n1;
-      if (v + CW * 32 < V) { n0 = __ldg(r0 + v + CW * 32); n1 = __ldg(r1 + v + CW * 32); }
+    for (int i = 0; i < AHEAD; ++i) {
+      double w[EB][8], f[8];
 #pragma unroll
-      for (int t0 = 0; t0 < TC; t0 += 8) {
-        uint4 x[8];                          // eight tokens' runs at once
+      for (int k = 0; k < EB; ++k) to_double8(we[i][k], w[k]);
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
-          if (t0 + t < a.T) x[t] = __ldg(ru + static_cast<size_t>(t0 + t) * V + v);
-        add(c0, c1, x, t0, a.T - t0);
-      }
+      for (int t = 0; t < TB; ++t)
+        if (t0 + t < a.T) {
+          to_double8(x[i][t], f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int k = 0; k < EB; ++k) acc[k * TB + t] = fma(f[j], w[k][j], acc[k * TB + t]);
+        }
     }
   }
-  // 2 TC sums over 32 lanes: each step halves the values a lane still holds
+  // M sums over 32 lanes: each step halves the values a lane still holds
   int o = 16;
 #pragma unroll
-  for (int n = TC; n >= 1; n >>= 1, o >>= 1) {
+  for (int n = M / 2; n >= 1; n >>= 1, o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int i = 0; i < n; ++i) {
@@ -275,27 +267,28 @@ __device__ __forceinline__ void affinities(const Args& a, Small* sm, int e0, int
   }
 #pragma unroll
   for (; o >= 1; o >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
-  constexpr int SPREAD = 32 / (2 * TC);      // lanes that hold the same sum
-  if (lane % SPREAD == 0) sm->dots[warp][lane / SPREAD] = acc[0];
-  named_bar_sync(1, CW * 32);
-  if (tid < 2 * TC) {
+  constexpr int SPREAD = 32 / M;             // lanes that hold the same sum
+  if (lane % SPREAD == 0) dots[warp][lane / SPREAD] = acc[0];
+  __syncthreads();
+  if (tid < M) {
     double z = 0.0;
 #pragma unroll
-    for (int w = 0; w < CW; ++w) z += sm->dots[w][tid];
-    const int t = tid % TC, ex = tid < TC ? e0 : e1;
-    if (t < a.T && ex >= 0) {
+    for (int w = 0; w < 8; ++w) z += dots[w][tid];
+    const int t = t0 + tid % TB, ex = e0 + tid / TB;
+    if (t < a.T && ex < a.N_r) {
       const float s = static_cast<float>(1.0 / (1.0 + exp(-z)));
       a.scores[t * a.N_r + ex] = make_float2(s + __ldg(a.b + ex), s);
     }
   }
-  named_bar_sync(1, CW * 32);
+  for (int i = block * 256 + tid; i < a.ctr_words; i += blocks * 256) a.slot_done[i] = 0u;
+  if (a.xq_ws != nullptr) quantise_u(a, block, blocks);
 }
 
 // 1x128 tiles of u by moe_quant_1x128's rule, half a warp a tile.
-__device__ __forceinline__ void quantise_u(const Args& a) {
-  const int half = (blockIdx.x * CW + (threadIdx.x >> 5)) * 2 + ((threadIdx.x >> 4) & 1);
+__device__ __forceinline__ void quantise_u(const Args& a, int block, int blocks) {
+  const int half = (block * 8 + (threadIdx.x >> 5)) * 2 + ((threadIdx.x >> 4) & 1);
   const int tiles = a.T * (a.d >> 7), sub = threadIdx.x & 15;
-  for (int first = half & ~1; first < tiles; first += gridDim.x * CW * 2) {
+  for (int first = half & ~1; first < tiles; first += blocks * 16) {
     const int tile = first + (half & 1);
     const bool live = tile < tiles;
     uint4 raw = make_uint4(0, 0, 0, 0);
@@ -323,6 +316,8 @@ __device__ __forceinline__ void quantise_u(const Args& a) {
   }
 }
 
+// ---------------------------------------------------------------- selection
+
 // An FP32 key as an unsigned integer of the same order; NaN below everything.
 __device__ __forceinline__ uint32_t ordered(float k) {
   if (!(k == k)) return 1u;
@@ -331,94 +326,93 @@ __device__ __forceinline__ uint32_t ordered(float k) {
 }
 
 // One warp: the K largest keys of a token, equal ones by the lower index;
-// lane k < K ends with the k-th expert and its affinity.
-__device__ __forceinline__ void select_token(const Args& a, int t, int& ex, float& s) {
+// lane k < K ends with the k-th expert and its affinity. score: MAX_N floats of
+// the warp's own.
+__device__ __forceinline__ void select_token(const Args& a, int t, float* score, int& ex, float& s) {
   const int lane = lane_id();
   uint32_t key[MAX_N / 32];
-  float sc[MAX_N / 32];
 #pragma unroll
   for (int j = 0; j < MAX_N / 32; ++j) {
     const int i = j * 32 + lane;
     const float2 v = i < a.N_r ? __ldcg(a.scores + t * a.N_r + i) : make_float2(0.0f, 0.0f);
-    sc[j] = v.y;
+    score[i] = v.y;
     key[j] = i < a.N_r ? ordered(v.x) : 0u;                          // 0: taken or absent
   }
   ex = 0;
-  s = 0.0f;
   for (int k = 0; k < a.K; ++k) {
-    uint32_t best = 0u;
-    int at = MAX_N;
-    float bs = 0.0f;
+    uint32_t best[4];
+    int at[4];
 #pragma unroll
-    for (int j = 0; j < MAX_N / 32; ++j)
-      if (key[j] > best) { best = key[j]; at = j * 32 + lane; bs = sc[j]; }
-    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    const int win = static_cast<int>(__reduce_min_sync(0xffffffffu, best == top ? static_cast<uint32_t>(at) : MAX_N));
-    const float ws = __shfl_sync(0xffffffffu, bs, win & 31);
-    if (lane == k) { ex = win; s = ws; }
+    for (int j = 0; j < 4; ++j) {            // the lane's best, by a tree; the left side wins ties
+      at[j] = key[2 * j + 1] > key[2 * j] ? 2 * j + 1 : 2 * j;
+      best[j] = max(key[2 * j], key[2 * j + 1]);
+    }
+    if (best[1] > best[0]) { best[0] = best[1]; at[0] = at[1]; }
+    if (best[3] > best[2]) { best[2] = best[3]; at[2] = at[3]; }
+    if (best[2] > best[0]) { best[0] = best[2]; at[0] = at[2]; }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best[0]);
+    const int win = static_cast<int>(
+        __reduce_min_sync(0xffffffffu, best[0] == top ? static_cast<uint32_t>(at[0] * 32 + lane) : MAX_N));
+    if (lane == k) ex = win;
 #pragma unroll
     for (int j = 0; j < MAX_N / 32; ++j)
       if (j * 32 + lane == win) key[j] = 0u;
   }
+  __syncwarp();
+  s = lane < a.K ? score[ex] : 0.0f;
 }
 
-// Every CTA selects for itself: slot 0 is the shared expert with every token,
+// Every CTA selects for itself (scores: CW * MAX_N floats of scratch): slot 0 is the shared expert with every token,
 // then the touched experts in ascending order, their tokens ascending.
-__device__ __forceinline__ void select_all(const Args& a, Small* sm) {
+__device__ __forceinline__ void select_all(const Args& a, Small* sm, float* scores) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int ex[2];
-  float g[2];
+  int ex[2] = {0, 0};
+  float g[2] = {0.0f, 0.0f};
+#pragma unroll
   for (int r = 0; r < 2; ++r) {
     const int t = warp + r * CW;
     if (t >= a.T) continue;
-    float s;
-    select_token(a, t, ex[r], s);
-    float sum = 0.0f;
-    for (int k = 0; k < a.K; ++k) sum += __shfl_sync(0xffffffffu, s, k);
-    g[r] = __fdiv_rn(s, sum);
-    if (lane < a.K) {
-      atomicOr(&sm->mask[ex[r]], 1u << t);
-      if (blockIdx.x == 0) {
-        a.topk_idx[t * a.K + lane] = ex[r];
-        a.gates[t * a.K + lane] = g[r];
-      }
-    }
-  }
-  named_bar_sync(1, CW * 32);
-  {                                          // a warp lists 32 experts; the chunks' totals join them
-    const int i = warp * 32 + lane;
-    const int n = i < a.N_r ? __popc(sm->mask[i]) : 0;
-    const uint32_t on = __ballot_sync(0xffffffffu, n > 0);
-    int pre = n;
+    select_token(a, t, scores + warp * MAX_N, ex[r], g[r]);
+    if (lane < a.K) atomicOr(&sm->mask[ex[r]], 1u << t);
+    float sum = g[r];                        // MAX_K lanes' affinities, those behind K zero
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, pre, o);
-      if (lane >= o) pre += v;
-    }
-    if (lane == 31) { sm->chunk_slots[warp] = __popc(on); sm->chunk_ents[warp] = pre; }
-    named_bar_sync(1, CW * 32);
-    int slots = 1, ents = a.T;
-    for (int w = 0; w < warp; ++w) { slots += sm->chunk_slots[w]; ents += sm->chunk_ents[w]; }
-    if (n > 0) {
-      const int s = slots + __popc(on & ((1u << lane) - 1u));
-      sm->slot_expert[s] = i;
-      sm->slot_of[i] = s;
-      sm->slot_start[s] = ents + pre - n;
-    }
-    if (blockIdx.x == 0 && a.counts != nullptr && i < a.N_r) a.counts[i] = n;
-    if (warp == CW - 1 && lane == 31) {
-      sm->slot_start[slots + __popc(on)] = ents + pre;
-      sm->n_slots = slots + __popc(on);
-      sm->slot_expert[0] = a.N_r;
-      sm->slot_start[0] = 0;
-    }
-    if (warp == 0 && lane < a.T) {
-      sm->ent_tok[lane] = lane;
-      sm->ent_row[lane] = a.T * a.K + lane;
-      sm->ent_gate[lane] = 1.0f;
-    }
+    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    g[r] = __fdiv_rn(g[r], sum);
   }
   named_bar_sync(1, CW * 32);
+  const int i = warp * 32 + lane;            // a warp lists 32 experts; the chunks' totals join them
+  const int n = i < a.N_r ? __popc(sm->mask[i]) : 0;
+  const uint32_t on = __ballot_sync(0xffffffffu, n > 0);
+  int pre = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, pre, o);
+    if (lane >= o) pre += v;
+  }
+  if (lane == 31) { sm->chunk_slots[warp] = __popc(on); sm->chunk_ents[warp] = pre; }
+  named_bar_sync(1, CW * 32);
+  int slots = 1, ents = a.T;
+  for (int w = 0; w < warp; ++w) { slots += sm->chunk_slots[w]; ents += sm->chunk_ents[w]; }
+  if (n > 0) {
+    const int s = slots + __popc(on & ((1u << lane) - 1u));
+    sm->slot_expert[s] = i;
+    sm->slot_of[i] = s;
+    sm->slot_start[s] = ents + pre - n;
+  }
+  if (warp == CW - 1 && lane == 31) {
+    sm->slot_start[slots + __popc(on)] = ents + pre;
+    sm->n_slots = slots + __popc(on);
+    sm->slot_expert[0] = a.N_r;
+    sm->slot_start[0] = 0;
+  }
+  named_bar_sync(1, CW * 32);
+  if (tid == 0) mbar_arrive(&sm->sel_ready); // the producer needs the slots alone
+  if (warp == 0 && lane < a.T) {
+    sm->ent_tok[lane] = lane;
+    sm->ent_row[lane] = a.T * a.K + lane;
+    sm->ent_gate[lane] = 1.0f;
+  }
+#pragma unroll
   for (int r = 0; r < 2; ++r) {
     const int t = warp + r * CW;
     if (t < a.T && lane < a.K) {
@@ -426,9 +420,13 @@ __device__ __forceinline__ void select_all(const Args& a, Small* sm) {
       sm->ent_tok[p] = t;
       sm->ent_row[p] = t * a.K + lane;
       sm->ent_gate[p] = g[r];
+      if (blockIdx.x == 0) {
+        a.topk_idx[t * a.K + lane] = ex[r];
+        a.gates[t * a.K + lane] = g[r];
+      }
     }
   }
-  named_bar_sync(1, CW * 32);
+  if (blockIdx.x == 0 && a.counts != nullptr && i < a.N_r) a.counts[i] = n;
 }
 
 // ---------------------------------------------------------------- work lists
@@ -487,6 +485,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
     for (int i = 0; i < BUFS; ++i) { mbar_init(&sm->tfull[i], 1); mbar_init(&sm->tempty[i], PW); }
     for (int i = 0; i < EW_MAX; ++i) { mbar_init(&sm->redfull[i], PW); mbar_init(&sm->redempty[i], 1); }
     mbar_init(&sm->sel_ready, 1);
+    mbar_init(&sm->x_ready, 1);
     mbar_init(&sm->x_free, MI);
     mbar_init(&sm->drained, MI);
     sm->abort = 0;
@@ -534,14 +533,15 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
         const int slots = sm->n_slots;
         for (; ok && unit < slots * per; unit += gridDim.x) gate_up(unit);
         const CUtensorMap* down = &maps.down[nrows & 1];
+        const int tile = STAGE / a.sk2;
         for (int si = 0; ok && si < slots; ++si) {
           const int row = sm->slot_expert[si] * a.d + row0;
-          for (int k = 0; k < kb_i; k += SK) {
+          for (int k = 0; k < kb_i; k += a.sk2) {
             if (!(ok = mbar_wait(&sm->empty[c.i], c.lap, abort))) break;
             uint64_t* bar = &sm->full[c.i];
-            const int nk = min(SK, kb_i - k);
+            const int nk = min(a.sk2, kb_i - k);
             mbar_arrive_expect_tx(bar, nk * nrows * 128);
-            for (int j = 0; j < nk; ++j) tma_load_2d(ring + c.i * STAGE + j * TILE, down, bar, (k + j) * 128, row);
+            for (int j = 0; j < nk; ++j) tma_load_2d(ring + c.i * STAGE + j * tile, down, bar, (k + j) * 128, row);
             ++issued;
             c.next(a.stages);
           }
@@ -553,23 +553,14 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
     }
   } else if (warp > CW) {
     // ------------------------------------------------------------ MMA issuers (the whole warp keeps step)
-    if (warp == CW + 1 && lane > 0) {                             // the shared expert's gate and up codes on their way into L2
-      const size_t bytes = static_cast<size_t>(a.I) * a.d, piece = 4096;
-      const size_t first = bytes / piece * blockIdx.x / gridDim.x, last = bytes / piece * (blockIdx.x + 1) / gridDim.x;
-      for (size_t i = first + lane - 1; i < last; i += 31) {
-        prefetch_l2(a.w_gate_shared + i * piece, piece);
-        prefetch_l2(a.w_up_shared + i * piece, piece);
-      }
-    }
-    __syncwarp();
-    constexpr uint32_t idesc = make_idesc(0, 0, 128, N);
-    bool ok = warp_wait(&sm->sel_ready, 0, abort);
+    bool ok = warp_wait(&sm->x_ready, 0, abort);
     Cursor c, t;
     t.lap = 1;
     int turn = warp - CW - 1;                   // stages until this warp's next one
-    // one stage against the two blocks of the token operand at tok. MMAs into one sum wait for each other:
-    // QS sums are interleaved.
-    auto stage = [&](const uint8_t* tok) {
+    // one stage against kn blocks of the token operand at tok: 128 / kn rows by kn blocks. MMAs into one sum
+    // wait for each other: qs sums are interleaved.
+    auto stage = [&](auto kn, auto qs, const uint8_t* tok) {
+      constexpr int NN = decltype(kn)::value * R, Q = decltype(qs)::value;
       if (turn-- > 0) {
         c.next(a.stages);
         t.next(BUFS);
@@ -584,7 +575,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
       const uint32_t dt = tmem + t.i * BUF_COLS;
       if (lane == 0) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) umma_f8f6f4(dt + (q % QS) * N, ad + 2 * q, bd + 2 * q, idesc, q >= QS);
+        for (int q = 0; q < 4; ++q)
+          umma_f8f6f4(dt + (q % Q) * NN, ad + 2 * q, bd + 2 * q, make_idesc(0, 0, 128, NN), q >= Q);
         umma_commit(&sm->empty[c.i]);
         umma_commit(&sm->tfull[t.i]);
       }
@@ -595,13 +587,17 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
     if (ok) {
       const int slots = sm->n_slots;
       for (int unit = blockIdx.x; ok && unit < slots * per; unit += gridDim.x)
-        for (int k = 0; ok && k < kb_d; k += SK) stage(xh + k * tile_bytes);
+        for (int k = 0; ok && k < kb_d; k += SK) stage(Int<SK>{}, Int<QS>{}, xh + k * tile_bytes);
       if (lane == 0) umma_commit(&sm->x_free);
       Cursor h;
       for (int si = 0; ok && si < slots; ++si) {
         ok = warp_wait(&sm->hfull[h.i], h.lap, abort);
         const uint8_t* hb = xh + h.i * a.hbuf_bytes;
-        for (int k = 0; ok && k < kb_i; k += SK) stage(hb + k * tile_bytes);
+        if (a.sk2 == SK) {
+          for (int k = 0; ok && k < kb_i; k += SK) stage(Int<SK>{}, Int<QS>{}, hb + k * tile_bytes);
+        } else {
+          for (int k = 0; ok && k < kb_i; k += 2 * SK) stage(Int<2 * SK>{}, Int<QS / 2>{}, hb + k * tile_bytes);
+        }
         if (lane == 0) umma_commit(&sm->hempty[h.i]);
         h.next(a.hbufs);
       }
@@ -612,47 +608,39 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------ router and selection
+    // ------------------------------------------------------------ selection and the tokens' operand
     const int tid = threadIdx.x;
-    if (a.xq_ws != nullptr) quantise_u(a);
-    for (int e0 = blockIdx.x; e0 < a.N_r; e0 += 2 * gridDim.x) {
-      const int e1 = e0 + static_cast<int>(gridDim.x) < a.N_r ? e0 + static_cast<int>(gridDim.x) : -1;
-      if (R == 8 && a.T <= LEAD) affinities<LEAD>(a, sm, e0, e1);
-      else affinities<R>(a, sm, e0, e1);
-    }
-    __threadfence();
-    named_bar_sync(1, CW * 32);
-    if (tid == 0) count_up(a.grid_ctr);
-    if (a.xq_ws == nullptr) stage_tokens<R>(a, xh, xs);       // given by the caller: no need to wait
-    if (tid == 0) count_wait(a.grid_ctr, gridDim.x, abort);
-    named_bar_sync(1, CW * 32);
-    if (a.xq_ws != nullptr) stage_tokens<R>(a, xh, xs);
+    select_all(a, sm, red);
+    stage_tokens<R>(a, xh, xs);
     fence_proxy_async_smem();
-    select_all(a, sm);
-    if (tid == 0) mbar_arrive(&sm->sel_ready);
+    named_bar_sync(1, CW * 32);
+    if (tid == 0) mbar_arrive(&sm->x_ready);
     const int slots = sm->n_slots, units = slots * per;
 
     if (warp < PW) {
       // ---------------------------------------------------------- sums of the partials: a thread owns a TMEM lane
       // first phase: lanes are 32 gate rows of block 0, of block 1, 32 up rows of block 0, of block 1;
-      // second phase: 64 rows of W_down in block 0, then in block 1
+      // second phase: 64 rows of W_down in block 0, then in block 1, or 32 rows in each of four blocks
       bool ok = true;
       Cursor t, e;
       e.lap = 1;
       // waits for the stage's partials; NC columns of this warp's quarter from column c0
       const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-      auto partials = [&](auto nc, int c0, float* v) {
-        constexpr int NC = decltype(nc)::value;
+      auto partials = [&](auto nc, auto kn, auto qs, int c0, float* v) {
+        constexpr int NC = decltype(nc)::value, NN = decltype(kn)::value * R, Q = decltype(qs)::value;
         ok = ok && warp_wait(&sm->tfull[t.i], t.lap, abort);
         if (ok) {
-          uint32_t r[QS * NC];
+          uint32_t r[Q * NC];
           tc_fence_after();
 #pragma unroll
-          for (int q = 0; q < QS; ++q) tmem_ld_async<NC>(taddr + t.i * BUF_COLS + q * N + c0, r + q * NC);
+          for (int q = 0; q < Q; ++q) tmem_ld_async<NC>(taddr + t.i * BUF_COLS + q * NN + c0, r + q * NC);
           tmem_wait_ld(r);
           tc_fence_before();
 #pragma unroll
-          for (int c = 0; c < NC; ++c) v[c] = __uint_as_float(r[c]) + __uint_as_float(r[NC + c]);
+          for (int c = 0; c < NC; ++c) {
+            v[c] = __uint_as_float(r[c]);
+            if constexpr (Q == 2) v[c] += __uint_as_float(r[NC + c]);
+          }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->tempty[t.i]);
@@ -677,7 +665,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
           for (int c = 0; c < R; ++c) acc[c] = 0.0f;
           for (int k = 0; k < kb_d; k += SK) {
             float v[R];
-            partials(std::integral_constant<int, R>{}, half * R, v);
+            partials(Int<R>{}, Int<SK>{}, Int<QS>{}, half * R, v);
             const float w = __shfl_sync(0xffffffffu, mine, k >> 1);
             const float* x = xs + (k + half) * COLS;
             if (ok) {
@@ -704,16 +692,17 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
       }
 
       // W_down: the CTA's rows over every slot, whose tokens are the first columns
-      const int half = warp >> 1;
-      const int r = (warp & 1) * 32 + lane;
+      const bool wide = a.sk2 != SK;            // four blocks a stage
+      const int kq = wide ? warp : warp >> 1;   // this warp's block of a stage
+      const int r = wide ? lane : (warp & 1) * 32 + lane;
       const int nb0 = row0 >> 7;                // rows of one or two 128-row blocks
       const bool upper = ((row0 + min(r, max(nrows - 1, 0))) >> 7) != nb0;
       float* sums = osum + warp * R * 32 + lane;
 #pragma unroll
       for (int c = 0; c < R; ++c) sums[c * 32] = 0.0f;
-      auto scales_of = [&](int si, float& lo, float& hi) {
+      auto scales_of = [&](int si, float& lo, float& hi) {     // lane i: of the warp's block of stage i
         const float* sw = a.s_down + (static_cast<size_t>(sm->slot_expert[si]) * kb_d + nb0) * kb_i;
-        const int kb = 2 * lane + half;
+        const int kb = a.sk2 * lane + kq;
         lo = hi = 0.0f;
         if (kb < kb_i) {
           lo = __ldg(sw + kb);
@@ -727,43 +716,52 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
         const float lo = next_lo, hi = next_hi;
         if (si + 1 < slots) scales_of(si + 1, next_lo, next_hi);
         ok = ok && warp_wait(&sm->hfull[h.i], h.lap, abort);
-        const float* hs = reinterpret_cast<const float*>(xh + h.i * a.hbuf_bytes + kb_i * tile_bytes);
+        const float* hs = reinterpret_cast<const float*>(xh + h.i * a.hbuf_bytes + kb_i * tile_bytes);   // [token][hs_pitch]
         const int first = sm->slot_start[si], ntok = sm->slot_start[si + 1] - first;
-        auto rows = [&](auto nc) {
-          constexpr int NC = decltype(nc)::value;
+        auto rows = [&](auto nc, auto kn, auto qs) {
+          constexpr int NC = decltype(nc)::value, KN = decltype(kn)::value;
           float acc[NC];
 #pragma unroll
           for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
-          for (int k = 0; k < kb_i; k += SK) {
+          for (int k = 0, n = 0; k < kb_i; k += KN, ++n) {
             float v[NC];
-            partials(nc, half * R, v);
-            const float wl = __shfl_sync(0xffffffffu, lo, k >> 1), wh = __shfl_sync(0xffffffffu, hi, k >> 1);
+            partials(nc, kn, qs, kq * R, v);
+            const float wl = __shfl_sync(0xffffffffu, lo, n), wh = __shfl_sync(0xffffffffu, hi, n);
             const float w = upper ? wh : wl;
-            if (ok && k + half < kb_i) {
+            if (ok && k + kq < kb_i) {
 #pragma unroll
-              for (int c = 0; c < NC; ++c) acc[c] = fmaf(v[c], hs[(k + half) * COLS + c] * w, acc[c]);
+              for (int c = 0; c < NC; ++c) acc[c] = fmaf(v[c], hs[c * a.hs_pitch + k + kq] * w, acc[c]);
             }
           }
 #pragma unroll
           for (int c = 0; c < NC; ++c)
-            if (c < ntok) sums[sm->ent_tok[first + c] * 32] += acc[c];
+            if (c < ntok) {
+              float* p = sums + sm->ent_tok[first + c] * 32;
+              *p = fmaf(acc[c], sm->ent_gate[first + c], *p);
+            }
         };
-        if (ntok <= 2) rows(std::integral_constant<int, 2>{});
-        else if (ntok <= 4) rows(std::integral_constant<int, 4>{});
-        else if (R == 8 || ntok <= 8) rows(std::integral_constant<int, 8>{});
-        else rows(std::integral_constant<int, R>{});
+        auto columns = [&](auto kn, auto qs) {
+          if (ntok <= 2) rows(Int<2>{}, kn, qs);
+          else if (ntok <= 4) rows(Int<4>{}, kn, qs);
+          else if (R == 8 || ntok <= 8) rows(Int<8>{}, kn, qs);
+          else rows(Int<R>{}, kn, qs);
+        };
+        if (wide) columns(Int<2 * SK>{}, Int<QS / 2>{});
+        else columns(Int<SK>{}, Int<QS>{});
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->hempty[h.i]);
         h.next(a.hbufs);
       }
-      // both blocks' sums, and the outputs
+      // the blocks' sums, and the outputs: a warp takes its rows' tokens in turn with the warps of the same rows
       named_bar_sync(3, PW * 32);
       const uint16_t* base = a.base != nullptr ? a.base : a.u;
       if (r < nrows)
-        for (int c = half; c < a.T; c += 2) {
+        for (int c = kq; c < a.T; c += a.sk2) {
           const size_t at = static_cast<size_t>(c) * a.d + row0 + r;
-          const float* p = osum + ((warp & 1) * R + c) * 32 + lane;
-          a.out[at] = float_to_bf16_bits(bf16_bits_to_float(base[at]) + (p[0] + p[2 * R * 32]));
+          const float* p = osum + c * 32 + lane;
+          constexpr int W = R * 32;             // from warp to warp
+          const float v = wide ? (p[0] + p[W]) + (p[2 * W] + p[3 * W]) : p[(warp & 1) * W] + p[((warp & 1) + 2) * W];
+          a.out[at] = float_to_bf16_bits(bf16_bits_to_float(base[at]) + v);
         }
     } else if (warp < PW + EW_MAX) {
       // ---------------------------------------------------------- finishing warps: SwiGLU, then the blocks' codes
@@ -799,7 +797,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
             const float s = tile_scale(amax);
             reinterpret_cast<uint32_t*>(a.hq + static_cast<size_t>(r) * a.I + blk * 128)[lane ^ ((j & 7) << 2)] =
                 e4m3x2(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s)) | (e4m3x2(__fdiv_rn(x.z, s), __fdiv_rn(x.w, s)) << 16);
-            if (lane == 0) a.hs[r * kb_i + blk] = s;
+            if (lane == 0) a.hs[r * a.hs_pitch + blk] = s;
           }
           fence_proxy_async_all();              // the codes are read by bulk copies
           __threadfence();
@@ -812,27 +810,30 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
       bool ok = warp_wait(&sm->x_free, 0, abort);
       Cursor h;
       h.lap = 1;
-      int si = 0;
+      int si = 0, done = 0;                     // slots before `done` are known to be quantised
       for (; ok && si < slots; ++si) {
         if (!(ok = warp_wait(&sm->hempty[h.i], h.lap, abort))) break;
-        int seen = 0;
-        if (lane == 0) seen = count_wait(a.slot_done + si, kb_i, abort);
-        if (!(ok = __shfl_sync(0xffffffffu, seen, 0) != 0)) break;
-        fence_proxy_async_all();
+        if (si >= done) {                       // look at the next 32 slots at once; wait for the first of them
+          int seen = 1;
+          if (lane == 0) seen = count_wait(a.slot_done + si, kb_i, abort);
+          if (!(ok = __shfl_sync(0xffffffffu, seen, 0) != 0)) break;
+          const bool there = lane == 0 || (si + lane < slots && count_now(a.slot_done + si + lane) >= static_cast<unsigned>(kb_i));
+          const uint32_t missing = ~__ballot_sync(0xffffffffu, there);
+          done = si + (missing ? __ffs(missing) - 1 : 32);
+          __syncwarp();
+          __threadfence();
+          fence_proxy_async_all();
+        }
         const int first = sm->slot_start[si], ntok = sm->slot_start[si + 1] - first;
         uint8_t* hb = xh + h.i * a.hbuf_bytes;
-        float* hs = reinterpret_cast<float*>(hb + kb_i * tile_bytes);
-        for (int o = lane; o < ntok * kb_i; o += 32) {
-          const int j = o / kb_i, k = o - j * kb_i;
-          hs[k * COLS + j] = __ldcg(a.hs + sm->ent_row[first + j] * kb_i + k) * sm->ent_gate[first + j];
-        }
+        if (lane == 0) mbar_arrive_expect_tx(&sm->hfull[h.i], ntok * (a.I + a.hs_pitch * 4));
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(&sm->hfull[h.i], ntok * a.I);
-        __syncwarp();
-        for (int o = lane; o < ntok * kb_i; o += 32) {
-          const int j = o / kb_i, k = o - j * kb_i;
-          bulk_load(hb + k * tile_bytes + j * 128,
-                    a.hq + static_cast<size_t>(sm->ent_row[first + j]) * a.I + k * 128, 128, &sm->hfull[h.i]);
+        for (int j = 0; j < ntok; ++j) {
+          const size_t row = sm->ent_row[first + j];
+          for (int k = lane; k < kb_i; k += 32)
+            bulk_load(hb + k * tile_bytes + j * 128, a.hq + row * a.I + k * 128, 128, &sm->hfull[h.i]);
+          if (lane == 31)
+            bulk_load(hb + kb_i * tile_bytes + j * a.hs_pitch * 4, a.hs + row * a.hs_pitch, a.hs_pitch * 4, &sm->hfull[h.i]);
         }
         h.next(a.hbufs);
       }
@@ -859,14 +860,14 @@ inline Layout layout(int T, int d, int N_r, int K_r, int I) {
   const size_t P = static_cast<size_t>(T) * K_r + T;
   const size_t slots = (T * K_r < N_r ? T * K_r : N_r) + 1;
   l.slots = slots;
-  l.ctr_bytes = 128 + slots * 4 + slots * (I / 128) * 4;
+  l.ctr_bytes = slots * 4 + slots * (I / 128) * 4;
   l.scores = round_up(l.ctr_bytes, 256);
   l.xq = round_up(l.scores + static_cast<size_t>(T) * N_r * 8, 256);
   l.xs = round_up(l.xq + static_cast<size_t>(T) * d, 256);
   l.act = round_up(l.xs + static_cast<size_t>(T) * (d / 128) * 4, 256);
   l.hq = round_up(l.act + P * I * 4, 256);
   l.hs = round_up(l.hq + P * I, 256);
-  l.total = round_up(l.hs + P * (I / 128) * 4, 256);
+  l.total = round_up(l.hs + P * round_up(I / 128, 4) * 4, 256);
   return l;
 }
 
@@ -889,7 +890,7 @@ int launch(const Maps& maps, Args& a, int G, cudaStream_t s) {
   // region; the ring gets what is left
   const int x_bytes = (a.d / 128) * R * 128;
   const int osum = Shape<R>::RED * 4;            // the outputs' sums, behind the H tiles
-  a.hbuf_bytes = static_cast<int>(round_up((a.I / 128) * (R * 128 + COLS * 4), 1024));
+  a.hbuf_bytes = static_cast<int>(round_up((a.I / 128) * R * 128 + R * a.hs_pitch * 4, 1024));
   const int h_bytes = (2 * a.hbuf_bytes <= 96 * 1024 ? 2 : 1) * a.hbuf_bytes + osum;
   a.xh_bytes = x_bytes > h_bytes ? x_bytes : h_bytes;
   a.hbufs = (a.xh_bytes - osum) / a.hbuf_bytes;
@@ -897,6 +898,7 @@ int launch(const Maps& maps, Args& a, int G, cudaStream_t s) {
   // short units (small d) need several finishing warps; with long ones one keeps up, and its buffer's
   // room goes to the ring
   a.ew = R == 16 && a.d > 4096 ? 1 : EW_MAX;
+  static_assert((R == 16 ? 1 : EW_MAX) * Shape<R>::RED >= CW * MAX_N, "the selection's scratch lies in the units' sums");
   const size_t rest = a.xh_bytes + (a.d / 128) * COLS * 4 + a.ew * Shape<R>::RED * 4 + sizeof(Small);
   a.stages = static_cast<int>((SMEM_MAX - rest) / STAGE);
   if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
@@ -968,17 +970,16 @@ extern "C" int moe_few_tokens(const uint16_t* u, const uint8_t* xq, const float*
   a.xs = xq ? xs : a.xs_ws;
   a.s_gate = s_gate; a.s_up = s_up; a.s_down = s_down;
   a.out = out; a.topk_idx = topk_idx; a.gates = gates; a.counts = counts;
-  a.grid_ctr = reinterpret_cast<unsigned*>(ws);
-  a.slot_done = reinterpret_cast<unsigned*>(ws + 128);
-  a.blk_ctr = reinterpret_cast<int*>(ws + 128 + l.slots * 4);
+  a.slot_done = reinterpret_cast<unsigned*>(ws);
+  a.blk_ctr = reinterpret_cast<int*>(ws + l.slots * 4);
+  a.ctr_words = static_cast<int>(l.ctr_bytes / 4);
+  a.hs_pitch = static_cast<int>(round_up(I / 128, 4));
+  a.sk2 = (d + G - 1) / G <= LIVE / 2 ? 2 * SK : SK;
   a.scores = reinterpret_cast<float2*>(ws + l.scores);
   a.act = reinterpret_cast<float*>(ws + l.act);
   a.hq = ws + l.hq;
   a.hs = reinterpret_cast<float*>(ws + l.hs);
   a.T = T; a.d = d; a.N_r = N_r; a.K = K_r; a.I = I;
-
-  a.w_gate_shared = w_gate + static_cast<size_t>(N_r) * I * d;
-  a.w_up_shared = w_up + static_cast<size_t>(N_r) * I * d;
 
   Maps maps;
   const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -989,6 +990,10 @@ extern "C" int moe_few_tokens(const uint16_t* u, const uint8_t* xq, const float*
     const int n = d / G + ((d / G) % 2 == i ? 0 : 1);
     if (int st = make_tmap_2d(&maps.down[i], w_down, U8, 1, slots * d, I, n > 0 ? n : 1, 128)) return st;
   }
-  if (int st = cuda_status(cudaMemsetAsync(ws, 0, l.ctr_bytes, s), "few tokens: counters")) return st;
+  if (T <= 4)
+    few_route_kernel<2, 4><<<dim3((N_r + 1) / 2, 1), 256, 0, s>>>(a);
+  else
+    few_route_kernel<4, 8><<<dim3((N_r + 3) / 4, (T + 7) / 8), 256, 0, s>>>(a);
+  if (int st = launch_status("few tokens: router launch")) return st;
   return T <= 8 ? launch<8>(maps, a, G, s) : launch<16>(maps, a, G, s);
 }
