@@ -33,10 +33,11 @@ constexpr int MAX_SLOTS = MAX_N + 1;
 constexpr int MAX_ENTRIES = MAX_T * MAX_K + MAX_T;
 constexpr int MAX_D = 8192;
 constexpr int CW = 8;                        // warps of the selection
-constexpr int EW_MAX = 3;                    // of them, finishing warps of the first phase
+constexpr int EW = 3;                    // of them, finishing warps of the first phase
 constexpr int PW = 4;                        // of them, warps that add up partials, one per 32 TMEM lanes
-constexpr int MI = 2;                        // MMA issuers, which take turns (stages and TMEM buffers are multiples of it)
-constexpr int THREADS = (CW + 1 + MI) * 32;  // and the producer
+constexpr int MI = 2;                        // producers, and MMA issuers: each kind takes turns, and the stages and
+                                             // TMEM buffers are multiples of it
+constexpr int THREADS = (CW + 2 * MI) * 32;
 constexpr int CH = 32;                       // intermediate channels of a unit
 constexpr int LIVE = 64;                     // live weight rows of a tile
 constexpr int SK = 2;                        // 128-channel blocks of a stage
@@ -47,6 +48,8 @@ constexpr int MAX_HBUF = 4;
 constexpr int COLS = 16;                     // a row of the scale tables
 constexpr int QS = 2;                        // sums of a block's four K = 32 steps: even and odd ones apart
 constexpr int BUFS = 8;                      // stages' partials in TMEM
+constexpr int MAX_GROUPS = 8;
+constexpr int MAX_MEMBERS = 256;             // and CTAs
 constexpr int SMEM_MAX = 227 * 1024;
 
 // Maps of the weights, rows [slot * rows] of codes, boxes of 128 channels by:
@@ -71,15 +74,18 @@ struct Args {
   int32_t* counts;
   unsigned* slot_done;      // [slot] quantised blocks of its H
   int* blk_ctr;             // [slot][I/128]: finished units of a block
+  int* join_ctr;            // [member] groups whose sums are written
   float2* scores;           // [T][N_r] key s + b, affinity s
+  float* part;              // [group][T][d] sums of a group's slots, with several groups
   float* act;               // [T*K + T][I] silu(G) U
   uint8_t* hq;              // [T*K + T][I] its codes, 16-byte words swizzled by place in the slot
   float* hs;                // [T*K + T][hs_pitch] its I/128 scales
   int T, d, N_r, K, I;
-  int sk2;                  // blocks of a second-phase stage: SK, or 2 SK where a CTA has at most 32 rows
-  int ctr_words;            // slot_done and blk_ctr, zeroed by the first kernel
+  int groups, members;      // second phase: groups of CTAs with a share of the slots each, rows split over a group's members
+  int ctr_words;            // slot_done, blk_ctr and join_ctr, zeroed by the first kernel
   int hs_pitch;             // I/128 rounded up to 4
-  int stages, hbufs, xh_bytes, hbuf_bytes, ew;   // ew: finishing warps, a buffer of sums each
+  int stages, hbufs, xh_bytes, hbuf_bytes;
+  int reds;                 // buffers of units' sums
 };
 
 // R: token rows of an operand tile (T rounded up to 8).
@@ -99,10 +105,10 @@ struct Small {
   uint64_t full[MAX_STAGES], empty[MAX_STAGES];
   uint64_t hfull[MAX_HBUF], hempty[MAX_HBUF];
   uint64_t tfull[BUFS], tempty[BUFS];
-  uint64_t redfull[EW_MAX], redempty[EW_MAX];
+  uint64_t redfull[EW], redempty[EW];
   uint64_t sel_ready, x_ready, x_free, drained;
   uint32_t tmem;
-  int abort;
+  int abort, last;
   int n_slots;
   uint32_t mask[MAX_N];                      // tokens of expert i
   uint16_t slot_expert[MAX_SLOTS];
@@ -470,9 +476,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
   uint8_t* ring = smem;
   uint8_t* xh = smem + static_cast<size_t>(a.stages) * STAGE;        // tokens' codes, then the H tiles
   float* xs = reinterpret_cast<float*>(xh + a.xh_bytes);             // [d/128][16]
-  float* red = xs + (a.d >> 7) * COLS;                               // [ew][PW][R][CH]
+  float* red = xs + (a.d >> 7) * COLS;                               // [reds][PW][R][CH]
   float* osum = reinterpret_cast<float*>(xh + a.hbufs * a.hbuf_bytes);   // [PW][R][32], in the second phase
-  Small* sm = reinterpret_cast<Small*>(red + a.ew * RED);
+  Small* sm = reinterpret_cast<Small*>(red + a.reds * RED);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kb_d = a.d >> 7, kb_i = a.I >> 7;
@@ -483,7 +489,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
     for (int i = 0; i < MAX_STAGES; ++i) { mbar_init(&sm->full[i], 1); mbar_init(&sm->empty[i], 1); }
     for (int i = 0; i < MAX_HBUF; ++i) { mbar_init(&sm->hfull[i], 1); mbar_init(&sm->hempty[i], MI + PW); }
     for (int i = 0; i < BUFS; ++i) { mbar_init(&sm->tfull[i], 1); mbar_init(&sm->tempty[i], PW); }
-    for (int i = 0; i < EW_MAX; ++i) { mbar_init(&sm->redfull[i], PW); mbar_init(&sm->redempty[i], 1); }
+    for (int i = 0; i < EW; ++i) { mbar_init(&sm->redfull[i], PW); mbar_init(&sm->redempty[i], 1); }
     mbar_init(&sm->sel_ready, 1);
     mbar_init(&sm->x_ready, 1);
     mbar_init(&sm->x_free, MI);
@@ -491,7 +497,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
     sm->abort = 0;
     fence_mbar_init();
   }
-  if (warp == CW + 1) {
+  if (warp == CW + MI) {
     tmem_alloc(&sm->tmem, Shape<R>::TMEM_COLS);
     tmem_relinquish();
   }
@@ -500,22 +506,35 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem = sm->tmem;
 
-  const int row0 = range_begin(blockIdx.x, a.d, gridDim.x);           // the CTA's rows of W_down
-  const int nrows = range_begin(blockIdx.x + 1, a.d, gridDim.x) - row0;
+  // second phase: the CTA's rows of W_down, for the slots group, group + groups, ..
+  const int group = blockIdx.x / a.members, member = blockIdx.x - group * a.members;
+  const int row0 = group < a.groups ? range_begin(member, a.d, a.members) : 0;
+  const int nrows = group < a.groups ? range_begin(member + 1, a.d, a.members) - row0 : 0;
   const int per = a.I / CH;
 
-  if (warp == CW) {
-    // ------------------------------------------------------------ producer
+  if (warp >= CW && warp < CW + MI) {
+    // ------------------------------------------------------------ producers
     if (lane == 0) {
       Cursor c;
+      int turn = warp - CW;                    // stages until this producer's next one
       c.lap = 1;                               // the first lap finds every stage empty
       int issued = 0;
       bool ok = true;
+      auto mine = [&] {                        // whether the next stage is; passes it if not
+        if (turn-- > 0) {
+          ++issued;
+          c.next(a.stages);
+          return false;
+        }
+        turn = MI - 1;
+        return true;
+      };
       auto gate_up = [&](int unit) {
         int slot, ch;
         unit_at(a, unit, slot, ch);
         const int row = (slot == 0 ? a.N_r : sm->slot_expert[slot]) * a.I + ch;
         for (int k = 0; k < kb_d; k += SK) {
+          if (!mine()) continue;
           if (!(ok = mbar_wait(&sm->empty[c.i], c.lap, abort))) return;
           uint64_t* bar = &sm->full[c.i];
           uint8_t* dst = ring + c.i * STAGE;
@@ -533,15 +552,15 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
         const int slots = sm->n_slots;
         for (; ok && unit < slots * per; unit += gridDim.x) gate_up(unit);
         const CUtensorMap* down = &maps.down[nrows & 1];
-        const int tile = STAGE / a.sk2;
-        for (int si = 0; ok && si < slots; ++si) {
+        for (int si = group; ok && nrows > 0 && si < slots; si += a.groups) {
           const int row = sm->slot_expert[si] * a.d + row0;
-          for (int k = 0; k < kb_i; k += a.sk2) {
+          for (int k = 0; k < kb_i; k += SK) {
+            if (!mine()) continue;
             if (!(ok = mbar_wait(&sm->empty[c.i], c.lap, abort))) break;
             uint64_t* bar = &sm->full[c.i];
-            const int nk = min(a.sk2, kb_i - k);
+            const int nk = min(SK, kb_i - k);
             mbar_arrive_expect_tx(bar, nk * nrows * 128);
-            for (int j = 0; j < nk; ++j) tma_load_2d(ring + c.i * STAGE + j * tile, down, bar, (k + j) * 128, row);
+            for (int j = 0; j < nk; ++j) tma_load_2d(ring + c.i * STAGE + j * TILE, down, bar, (k + j) * 128, row);
             ++issued;
             c.next(a.stages);
           }
@@ -549,18 +568,18 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
       }
       // no copy may be in flight when the CTA ends
       for (int j = max(0, issued - a.stages); j < issued; ++j)
-        mbar_wait(&sm->full[j % a.stages], (j / a.stages) & 1, abort);
+        if (j % MI == warp - CW) mbar_wait(&sm->full[j % a.stages], (j / a.stages) & 1, abort);
     }
-  } else if (warp > CW) {
+  } else if (warp >= CW + MI) {
     // ------------------------------------------------------------ MMA issuers (the whole warp keeps step)
     bool ok = warp_wait(&sm->x_ready, 0, abort);
     Cursor c, t;
     t.lap = 1;
-    int turn = warp - CW - 1;                   // stages until this warp's next one
-    // one stage against kn blocks of the token operand at tok: 128 / kn rows by kn blocks. MMAs into one sum
-    // wait for each other: qs sums are interleaved.
-    auto stage = [&](auto kn, auto qs, const uint8_t* tok) {
-      constexpr int NN = decltype(kn)::value * R, Q = decltype(qs)::value;
+    int turn = warp - CW - MI;                  // stages until this warp's next one
+    // one stage against the two blocks of the token operand at tok. MMAs into one sum wait for each other:
+    // QS sums are interleaved.
+    constexpr uint32_t idesc = make_idesc(0, 0, 128, N);
+    auto stage = [&](const uint8_t* tok) {
       if (turn-- > 0) {
         c.next(a.stages);
         t.next(BUFS);
@@ -575,8 +594,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
       const uint32_t dt = tmem + t.i * BUF_COLS;
       if (lane == 0) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          umma_f8f6f4(dt + (q % Q) * NN, ad + 2 * q, bd + 2 * q, make_idesc(0, 0, 128, NN), q >= Q);
+        for (int q = 0; q < 4; ++q) umma_f8f6f4(dt + (q % QS) * N, ad + 2 * q, bd + 2 * q, idesc, q >= QS);
         umma_commit(&sm->empty[c.i]);
         umma_commit(&sm->tfull[t.i]);
       }
@@ -587,17 +605,13 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
     if (ok) {
       const int slots = sm->n_slots;
       for (int unit = blockIdx.x; ok && unit < slots * per; unit += gridDim.x)
-        for (int k = 0; ok && k < kb_d; k += SK) stage(Int<SK>{}, Int<QS>{}, xh + k * tile_bytes);
+        for (int k = 0; ok && k < kb_d; k += SK) stage(xh + k * tile_bytes);
       if (lane == 0) umma_commit(&sm->x_free);
       Cursor h;
-      for (int si = 0; ok && si < slots; ++si) {
+      for (int si = group; ok && nrows > 0 && si < slots; si += a.groups) {
         ok = warp_wait(&sm->hfull[h.i], h.lap, abort);
         const uint8_t* hb = xh + h.i * a.hbuf_bytes;
-        if (a.sk2 == SK) {
-          for (int k = 0; ok && k < kb_i; k += SK) stage(Int<SK>{}, Int<QS>{}, hb + k * tile_bytes);
-        } else {
-          for (int k = 0; ok && k < kb_i; k += 2 * SK) stage(Int<2 * SK>{}, Int<QS / 2>{}, hb + k * tile_bytes);
-        }
+        for (int k = 0; ok && k < kb_i; k += SK) stage(hb + k * tile_bytes);
         if (lane == 0) umma_commit(&sm->hempty[h.i]);
         h.next(a.hbufs);
       }
@@ -620,27 +634,25 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
     if (warp < PW) {
       // ---------------------------------------------------------- sums of the partials: a thread owns a TMEM lane
       // first phase: lanes are 32 gate rows of block 0, of block 1, 32 up rows of block 0, of block 1;
-      // second phase: 64 rows of W_down in block 0, then in block 1, or 32 rows in each of four blocks
+      // second phase: 64 rows of W_down in block 0, then in block 1
       bool ok = true;
       Cursor t, e;
       e.lap = 1;
+      int fin = 0;                              // the finishing warp of the unit at hand
       // waits for the stage's partials; NC columns of this warp's quarter from column c0
       const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-      auto partials = [&](auto nc, auto kn, auto qs, int c0, float* v) {
-        constexpr int NC = decltype(nc)::value, NN = decltype(kn)::value * R, Q = decltype(qs)::value;
+      auto partials = [&](auto nc, int c0, float* v) {
+        constexpr int NC = decltype(nc)::value;
         ok = ok && warp_wait(&sm->tfull[t.i], t.lap, abort);
         if (ok) {
-          uint32_t r[Q * NC];
+          uint32_t r[QS * NC];
           tc_fence_after();
 #pragma unroll
-          for (int q = 0; q < Q; ++q) tmem_ld_async<NC>(taddr + t.i * BUF_COLS + q * NN + c0, r + q * NC);
+          for (int q = 0; q < QS; ++q) tmem_ld_async<NC>(taddr + t.i * BUF_COLS + q * N + c0, r + q * NC);
           tmem_wait_ld(r);
           tc_fence_before();
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            v[c] = __uint_as_float(r[c]);
-            if constexpr (Q == 2) v[c] += __uint_as_float(r[NC + c]);
-          }
+          for (int c = 0; c < NC; ++c) v[c] = __uint_as_float(r[c]) + __uint_as_float(r[NC + c]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->tempty[t.i]);
@@ -665,7 +677,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
           for (int c = 0; c < R; ++c) acc[c] = 0.0f;
           for (int k = 0; k < kb_d; k += SK) {
             float v[R];
-            partials(Int<R>{}, Int<SK>{}, Int<QS>{}, half * R, v);
+            partials(Int<R>{}, half * R, v);
             const float w = __shfl_sync(0xffffffffu, mine, k >> 1);
             const float* x = xs + (k + half) * COLS;
             if (ok) {
@@ -686,15 +698,15 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
             for (int c = 0; c < R; ++c) p[c * CH] = acc[c];
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm->redfull[e.i]);
-          e.next(a.ew);
+          if (lane == 0) mbar_arrive(&sm->redfull[fin]);
+          fin = fin + 1 == EW ? 0 : fin + 1;
+          e.next(a.reds);
         }
       }
 
       // W_down: the CTA's rows over every slot, whose tokens are the first columns
-      const bool wide = a.sk2 != SK;            // four blocks a stage
-      const int kq = wide ? warp : warp >> 1;   // this warp's block of a stage
-      const int r = wide ? lane : (warp & 1) * 32 + lane;
+      const int kq = warp >> 1;                 // this warp's block of a stage
+      const int r = (warp & 1) * 32 + lane;
       const int nb0 = row0 >> 7;                // rows of one or two 128-row blocks
       const bool upper = ((row0 + min(r, max(nrows - 1, 0))) >> 7) != nb0;
       float* sums = osum + warp * R * 32 + lane;
@@ -702,7 +714,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
       for (int c = 0; c < R; ++c) sums[c * 32] = 0.0f;
       auto scales_of = [&](int si, float& lo, float& hi) {     // lane i: of the warp's block of stage i
         const float* sw = a.s_down + (static_cast<size_t>(sm->slot_expert[si]) * kb_d + nb0) * kb_i;
-        const int kb = a.sk2 * lane + kq;
+        const int kb = SK * lane + kq;
         lo = hi = 0.0f;
         if (kb < kb_i) {
           lo = __ldg(sw + kb);
@@ -711,21 +723,21 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
       };
       Cursor h;
       float next_lo, next_hi;
-      scales_of(0, next_lo, next_hi);
-      for (int si = 0; si < slots; ++si) {
+      scales_of(min(group, slots - 1), next_lo, next_hi);
+      for (int si = group; nrows > 0 && si < slots; si += a.groups) {
         const float lo = next_lo, hi = next_hi;
-        if (si + 1 < slots) scales_of(si + 1, next_lo, next_hi);
+        if (si + a.groups < slots) scales_of(si + a.groups, next_lo, next_hi);
         ok = ok && warp_wait(&sm->hfull[h.i], h.lap, abort);
         const float* hs = reinterpret_cast<const float*>(xh + h.i * a.hbuf_bytes + kb_i * tile_bytes);   // [token][hs_pitch]
         const int first = sm->slot_start[si], ntok = sm->slot_start[si + 1] - first;
-        auto rows = [&](auto nc, auto kn, auto qs) {
-          constexpr int NC = decltype(nc)::value, KN = decltype(kn)::value;
+        auto rows = [&](auto nc) {
+          constexpr int NC = decltype(nc)::value;
           float acc[NC];
 #pragma unroll
           for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
-          for (int k = 0, n = 0; k < kb_i; k += KN, ++n) {
+          for (int k = 0, n = 0; k < kb_i; k += SK, ++n) {
             float v[NC];
-            partials(nc, kn, qs, kq * R, v);
+            partials(nc, kq * R, v);
             const float wl = __shfl_sync(0xffffffffu, lo, n), wh = __shfl_sync(0xffffffffu, hi, n);
             const float w = upper ? wh : wl;
             if (ok && k + kq < kb_i) {
@@ -740,46 +752,61 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
               *p = fmaf(acc[c], sm->ent_gate[first + c], *p);
             }
         };
-        auto columns = [&](auto kn, auto qs) {
-          if (ntok <= 2) rows(Int<2>{}, kn, qs);
-          else if (ntok <= 4) rows(Int<4>{}, kn, qs);
-          else if (R == 8 || ntok <= 8) rows(Int<8>{}, kn, qs);
-          else rows(Int<R>{}, kn, qs);
-        };
-        if (wide) columns(Int<2 * SK>{}, Int<QS / 2>{});
-        else columns(Int<SK>{}, Int<QS>{});
+        if (ntok <= 2) rows(Int<2>{});
+        else if (ntok <= 4) rows(Int<4>{});
+        else if (R == 8 || ntok <= 8) rows(Int<8>{});
+        else rows(Int<R>{});
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->hempty[h.i]);
         h.next(a.hbufs);
       }
-      // the blocks' sums, and the outputs: a warp takes its rows' tokens in turn with the warps of the same rows
+      // both blocks' sums: the outputs with one group, else this group's share of them, and whoever writes a
+      // member's last share adds them up in the groups' order
       named_bar_sync(3, PW * 32);
       const uint16_t* base = a.base != nullptr ? a.base : a.u;
+      constexpr int W = R * 32;                 // from warp to warp
       if (r < nrows)
-        for (int c = kq; c < a.T; c += a.sk2) {
+        for (int c = kq; c < a.T; c += SK) {
           const size_t at = static_cast<size_t>(c) * a.d + row0 + r;
-          const float* p = osum + c * 32 + lane;
-          constexpr int W = R * 32;             // from warp to warp
-          const float v = wide ? (p[0] + p[W]) + (p[2 * W] + p[3 * W]) : p[(warp & 1) * W] + p[((warp & 1) + 2) * W];
-          a.out[at] = float_to_bf16_bits(bf16_bits_to_float(base[at]) + v);
+          const float* p = osum + (warp & 1) * W + c * 32 + lane;
+          const float v = p[0] + p[2 * W];
+          if (a.groups == 1) a.out[at] = float_to_bf16_bits(bf16_bits_to_float(base[at]) + v);
+          else a.part[static_cast<size_t>(group) * a.T * a.d + at] = v;
         }
-    } else if (warp < PW + EW_MAX) {
+      if (a.groups > 1 && nrows > 0) {
+        __threadfence();
+        named_bar_sync(3, PW * 32);
+        if (tid == 0) sm->last = atomicAdd(a.join_ctr + member, 1) == a.groups - 1;
+        named_bar_sync(3, PW * 32);
+        if (sm->last && r < nrows) {
+          __threadfence();
+          for (int c = kq; c < a.T; c += SK) {
+            const size_t at = static_cast<size_t>(c) * a.d + row0 + r;
+            float v = bf16_bits_to_float(base[at]);
+            for (int i = 0; i < a.groups; ++i) v += __ldcg(a.part + static_cast<size_t>(i) * a.T * a.d + at);
+            a.out[at] = float_to_bf16_bits(v);
+          }
+        }
+      }
+    } else if (warp < PW + EW) {
       // ---------------------------------------------------------- finishing warps: SwiGLU, then the blocks' codes
       const int e = warp - PW;
       uint32_t lap = 0;
-      for (int unit = blockIdx.x + e * gridDim.x; e < a.ew && unit < units; unit += a.ew * gridDim.x, lap ^= 1) {
+      int n = e;                                // the CTA's n-th unit
+      for (int unit = blockIdx.x + e * gridDim.x; unit < units; unit += EW * gridDim.x, lap ^= 1, n += EW) {
         if (!warp_wait(&sm->redfull[e], lap, abort)) break;
+        const int buf = n % a.reds;
         int slot, ch;
         unit_at(a, unit, slot, ch);
         const int first = sm->slot_start[slot], ntok = sm->slot_start[slot + 1] - first;
-        const float* p = red + e * RED + lane;
+        const float* p = red + buf * RED + lane;
         for (int j = 0; j < ntok; ++j) {
           const int t = sm->ent_tok[first + j];
           const float g = p[t * CH] + p[(R + t) * CH], u = p[(2 * R + t) * CH] + p[(3 * R + t) * CH];
           a.act[static_cast<size_t>(sm->ent_row[first + j]) * a.I + ch + lane] = __fdiv_rn(g, 1.0f + expf(-g)) * u;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->redempty[e]);
+        if (lane == 0) mbar_arrive(&sm->redempty[buf]);
         // the warp that finishes a 128-block last quantises it
         __threadfence();
         __syncwarp();
@@ -788,16 +815,27 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
         if (lane == 0) last = atomicAdd(a.blk_ctr + slot * kb_i + blk, 1) == 128 / CH - 1;
         if (__shfl_sync(0xffffffffu, last, 0)) {
           __threadfence();
-          for (int j = 0; j < ntok; ++j) {
-            const int r = sm->ent_row[first + j];
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(a.act + static_cast<size_t>(r) * a.I + blk * 128) + lane);
-            float amax = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+          for (int j0 = 0; j0 < ntok; j0 += 4) {         // four rows' loads in flight
+            float4 x[4];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const float s = tile_scale(amax);
-            reinterpret_cast<uint32_t*>(a.hq + static_cast<size_t>(r) * a.I + blk * 128)[lane ^ ((j & 7) << 2)] =
-                e4m3x2(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s)) | (e4m3x2(__fdiv_rn(x.z, s), __fdiv_rn(x.w, s)) << 16);
-            if (lane == 0) a.hs[r * a.hs_pitch + blk] = s;
+            for (int i = 0; i < 4; ++i)
+              x[i] = __ldcg(reinterpret_cast<const float4*>(
+                                a.act + static_cast<size_t>(sm->ent_row[first + min(j0 + i, ntok - 1)]) * a.I + blk * 128) + lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int j = j0 + i;
+              float amax = fmaxf(fmaxf(fabsf(x[i].x), fabsf(x[i].y)), fmaxf(fabsf(x[i].z), fabsf(x[i].w)));
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+              const float s = tile_scale(amax);
+              if (j < ntok) {
+                const size_t r = sm->ent_row[first + j];
+                reinterpret_cast<uint32_t*>(a.hq + r * a.I + blk * 128)[lane ^ ((j & 7) << 2)] =
+                    e4m3x2(__fdiv_rn(x[i].x, s), __fdiv_rn(x[i].y, s)) |
+                    (e4m3x2(__fdiv_rn(x[i].z, s), __fdiv_rn(x[i].w, s)) << 16);
+                if (lane == 0) a.hs[r * a.hs_pitch + blk] = s;
+              }
+            }
           }
           fence_proxy_async_all();              // the codes are read by bulk copies
           __threadfence();
@@ -805,21 +843,22 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
           if (lane == 0) count_up(a.slot_done + slot);
         }
       }
-    } else if (warp == PW + EW_MAX) {
+    } else if (warp == PW + EW) {
       // ---------------------------------------------------------- loader of the H tiles, over the tokens' operand
       bool ok = warp_wait(&sm->x_free, 0, abort);
       Cursor h;
       h.lap = 1;
-      int si = 0, done = 0;                     // slots before `done` are known to be quantised
-      for (; ok && si < slots; ++si) {
+      int n = 0, done = 0;                      // slots taken; those before `done` (in turn) are known to be quantised
+      for (int si = group; ok && nrows > 0 && si < slots; si += a.groups, ++n) {
         if (!(ok = warp_wait(&sm->hempty[h.i], h.lap, abort))) break;
-        if (si >= done) {                       // look at the next 32 slots at once; wait for the first of them
+        if (n >= done) {                        // look at the next 32 slots at once; wait for the first of them
           int seen = 1;
           if (lane == 0) seen = count_wait(a.slot_done + si, kb_i, abort);
           if (!(ok = __shfl_sync(0xffffffffu, seen, 0) != 0)) break;
-          const bool there = lane == 0 || (si + lane < slots && count_now(a.slot_done + si + lane) >= static_cast<unsigned>(kb_i));
+          const int at = si + lane * a.groups;
+          const bool there = lane == 0 || (at < slots && count_now(a.slot_done + at) >= static_cast<unsigned>(kb_i));
           const uint32_t missing = ~__ballot_sync(0xffffffffu, there);
-          done = si + (missing ? __ffs(missing) - 1 : 32);
+          done = n + (missing ? __ffs(missing) - 1 : 32);
           __syncwarp();
           __threadfence();
           fence_proxy_async_all();
@@ -837,12 +876,12 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
         }
         h.next(a.hbufs);
       }
-      for (int j = max(0, si - a.hbufs); j < si; ++j) mbar_wait(&sm->hfull[j % a.hbufs], (j / a.hbufs) & 1, abort);
+      for (int j = max(0, n - a.hbufs); j < n; ++j) mbar_wait(&sm->hfull[j % a.hbufs], (j / a.hbufs) & 1, abort);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == CW + 1) {
+  if (warp == CW + MI) {
     tc_fence_after();
     tmem_dealloc(tmem, Shape<R>::TMEM_COLS);
   }
@@ -853,18 +892,19 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
 inline size_t round_up(size_t n, size_t m) { return (n + m - 1) / m * m; }
 
 struct Layout {
-  size_t slots, ctr_bytes, scores, xq, xs, act, hq, hs, total;
+  size_t slots, ctr_bytes, scores, xq, xs, part, act, hq, hs, total;
 };
 inline Layout layout(int T, int d, int N_r, int K_r, int I) {
   Layout l;
   const size_t P = static_cast<size_t>(T) * K_r + T;
   const size_t slots = (T * K_r < N_r ? T * K_r : N_r) + 1;
   l.slots = slots;
-  l.ctr_bytes = slots * 4 + slots * (I / 128) * 4;
+  l.ctr_bytes = (slots + slots * (I / 128) + MAX_MEMBERS) * 4;
   l.scores = round_up(l.ctr_bytes, 256);
   l.xq = round_up(l.scores + static_cast<size_t>(T) * N_r * 8, 256);
   l.xs = round_up(l.xq + static_cast<size_t>(T) * d, 256);
-  l.act = round_up(l.xs + static_cast<size_t>(T) * (d / 128) * 4, 256);
+  l.part = round_up(l.xs + static_cast<size_t>(T) * (d / 128) * 4, 256);
+  l.act = round_up(l.part + static_cast<size_t>(MAX_GROUPS) * T * d * 4, 256);
   l.hq = round_up(l.act + P * I * 4, 256);
   l.hs = round_up(l.hq + P * I, 256);
   l.total = round_up(l.hs + P * round_up(I / 128, 4) * 4, 256);
@@ -891,15 +931,16 @@ int launch(const Maps& maps, Args& a, int G, cudaStream_t s) {
   const int x_bytes = (a.d / 128) * R * 128;
   const int osum = Shape<R>::RED * 4;            // the outputs' sums, behind the H tiles
   a.hbuf_bytes = static_cast<int>(round_up((a.I / 128) * R * 128 + R * a.hs_pitch * 4, 1024));
-  const int h_bytes = (2 * a.hbuf_bytes <= 96 * 1024 ? 2 : 1) * a.hbuf_bytes + osum;
+  const int want = 4 * a.hbuf_bytes <= 72 * 1024 ? 4 : 2 * a.hbuf_bytes <= 96 * 1024 ? 2 : 1;
+  const int h_bytes = want * a.hbuf_bytes + osum;
   a.xh_bytes = x_bytes > h_bytes ? x_bytes : h_bytes;
   a.hbufs = (a.xh_bytes - osum) / a.hbuf_bytes;
   if (a.hbufs > MAX_HBUF) a.hbufs = MAX_HBUF;
-  // short units (small d) need several finishing warps; with long ones one keeps up, and its buffer's
-  // room goes to the ring
-  a.ew = R == 16 && a.d > 4096 ? 1 : EW_MAX;
-  static_assert((R == 16 ? 1 : EW_MAX) * Shape<R>::RED >= CW * MAX_N, "the selection's scratch lies in the units' sums");
-  const size_t rest = a.xh_bytes + (a.d / 128) * COLS * 4 + a.ew * Shape<R>::RED * 4 + sizeof(Small);
+  // short units (small d) need several buffers of sums; with long ones one will do, and the others' room
+  // goes to the ring
+  a.reds = R == 16 && a.d > 4096 ? 1 : EW;
+  static_assert((R == 16 ? 1 : EW) * Shape<R>::RED >= CW * MAX_N, "the selection's scratch lies in the units' sums");
+  const size_t rest = a.xh_bytes + (a.d / 128) * COLS * 4 + a.reds * Shape<R>::RED * 4 + sizeof(Small);
   a.stages = static_cast<int>((SMEM_MAX - rest) / STAGE);
   if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
   a.stages -= a.stages % MI;                     // an issuer owns its stages: it never waits for another's lap
@@ -958,8 +999,8 @@ extern "C" int moe_few_tokens(const uint16_t* u, const uint8_t* xq, const float*
   MOE_CHECK_ARG(all % 16 == 0);
   DeviceInfo di;
   if (int st = device_info(&di)) return st;
-  const int G = di.sm_count;
-  if ((d + G - 1) / G > LIVE) return record_failure(MOE_ERR_UNSUPPORTED, "moe_few_tokens", "too few SMs for d");
+  const int G = di.sm_count < MAX_MEMBERS ? di.sm_count : MAX_MEMBERS;
+  if ((d + LIVE - 1) / LIVE > G) return record_failure(MOE_ERR_UNSUPPORTED, "moe_few_tokens", "too few SMs for d");
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   Args a{};
@@ -974,7 +1015,14 @@ extern "C" int moe_few_tokens(const uint16_t* u, const uint8_t* xq, const float*
   a.blk_ctr = reinterpret_cast<int*>(ws + l.slots * 4);
   a.ctr_words = static_cast<int>(l.ctr_bytes / 4);
   a.hs_pitch = static_cast<int>(round_up(I / 128, 4));
-  a.sk2 = (d + G - 1) / G <= LIVE / 2 ? 2 * SK : SK;
+  a.join_ctr = a.blk_ctr + l.slots * (I / 128);
+  a.part = reinterpret_cast<float*>(ws + l.part);
+  // With small d a CTA's rows of W_down would be few, and what a slot costs besides its bytes (about 0.7 us)
+  // would count: as many groups of CTAs as still leave 64 rows a member then share the slots. At d = 2048,
+  // I = 1024, 13 tokens, the second phase takes 48 us with one group.
+  a.groups = G / ((d + LIVE - 1) / LIVE);
+  if (a.groups > MAX_GROUPS) a.groups = MAX_GROUPS;
+  a.members = G / a.groups;
   a.scores = reinterpret_cast<float2*>(ws + l.scores);
   a.act = reinterpret_cast<float*>(ws + l.act);
   a.hq = ws + l.hq;
@@ -986,8 +1034,8 @@ extern "C" int moe_few_tokens(const uint16_t* u, const uint8_t* xq, const float*
   const uint64_t slots = static_cast<uint64_t>(N_r) + 1;
   if (int st = make_map(&maps.gate, w_gate, slots * I, d)) return st;
   if (int st = make_map(&maps.up, w_up, slots * I, d)) return st;
-  for (int i = 0; i < 2; ++i) {          // CTAs own d / G rows or one more: one count is even, one odd
-    const int n = d / G + ((d / G) % 2 == i ? 0 : 1);
+  for (int i = 0; i < 2; ++i) {          // members own d / members rows or one more: one count is even, one odd
+    const int q = d / a.members, n = q + (q % 2 == i ? 0 : 1);
     if (int st = make_tmap_2d(&maps.down[i], w_down, U8, 1, slots * d, I, n > 0 ? n : 1, 128)) return st;
   }
   if (T <= 4)
