@@ -77,9 +77,9 @@ struct Args {
   int* join_ctr;            // [member] groups whose sums are written
   float2* scores;           // [T][N_r] key s + b, affinity s
   float* part;              // [group][T][d] sums of a group's slots, with several groups
-  float* act;               // [T*K + T][I] silu(G) U
-  uint8_t* hq;              // [T*K + T][I] its codes, 16-byte words swizzled by place in the slot
-  float* hs;                // [T*K + T][hs_pitch] its I/128 scales
+  float* act;               // [entry][I] silu(G) U; entries are the slots' tokens, slot after slot
+  uint8_t* hq;              // its codes, a slot's as [I/128][tokens][128] with the operand tiles' swizzle
+  float* hs;                // [entry][hs_pitch] its I/128 scales
   int T, d, N_r, K, I;
   int groups, members;      // second phase: groups of CTAs with a share of the slots each, rows split over a group's members
   int ctr_words;            // slot_done, blk_ctr and join_ctr, zeroed by the first kernel
@@ -114,7 +114,6 @@ struct Small {
   uint16_t slot_expert[MAX_SLOTS];
   uint16_t slot_of[MAX_N];
   uint16_t slot_start[MAX_SLOTS + 1];
-  uint16_t ent_row[MAX_ENTRIES];             // row of act, hq and hs
   uint8_t ent_tok[MAX_ENTRIES];
   float ent_gate[MAX_ENTRIES];
   int chunk_slots[CW], chunk_ents[CW];
@@ -415,7 +414,6 @@ __device__ __forceinline__ void select_all(const Args& a, Small* sm, float* scor
   if (tid == 0) mbar_arrive(&sm->sel_ready); // the producer needs the slots alone
   if (warp == 0 && lane < a.T) {
     sm->ent_tok[lane] = lane;
-    sm->ent_row[lane] = a.T * a.K + lane;
     sm->ent_gate[lane] = 1.0f;
   }
 #pragma unroll
@@ -424,7 +422,6 @@ __device__ __forceinline__ void select_all(const Args& a, Small* sm, float* scor
     if (t < a.T && lane < a.K) {
       const int p = sm->slot_start[sm->slot_of[ex[r]]] + __popc(sm->mask[ex[r]] & ((1u << t) - 1u));
       sm->ent_tok[p] = t;
-      sm->ent_row[p] = t * a.K + lane;
       sm->ent_gate[p] = g[r];
       if (blockIdx.x == 0) {
         a.topk_idx[t * a.K + lane] = ex[r];
@@ -803,7 +800,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
         for (int j = 0; j < ntok; ++j) {
           const int t = sm->ent_tok[first + j];
           const float g = p[t * CH] + p[(R + t) * CH], u = p[(2 * R + t) * CH] + p[(3 * R + t) * CH];
-          a.act[static_cast<size_t>(sm->ent_row[first + j]) * a.I + ch + lane] = __fdiv_rn(g, 1.0f + expf(-g)) * u;
+          a.act[static_cast<size_t>(first + j) * a.I + ch + lane] = __fdiv_rn(g, 1.0f + expf(-g)) * u;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->redempty[buf]);
@@ -820,7 +817,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               x[i] = __ldcg(reinterpret_cast<const float4*>(
-                                a.act + static_cast<size_t>(sm->ent_row[first + min(j0 + i, ntok - 1)]) * a.I + blk * 128) + lane);
+                                a.act + static_cast<size_t>(first + min(j0 + i, ntok - 1)) * a.I + blk * 128) + lane);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int j = j0 + i;
@@ -829,11 +826,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
               for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
               const float s = tile_scale(amax);
               if (j < ntok) {
-                const size_t r = sm->ent_row[first + j];
-                reinterpret_cast<uint32_t*>(a.hq + r * a.I + blk * 128)[lane ^ ((j & 7) << 2)] =
+                reinterpret_cast<uint32_t*>(a.hq + static_cast<size_t>(first) * a.I + (blk * ntok + j) * 128)[lane ^ ((j & 7) << 2)] =
                     e4m3x2(__fdiv_rn(x[i].x, s), __fdiv_rn(x[i].y, s)) |
                     (e4m3x2(__fdiv_rn(x[i].z, s), __fdiv_rn(x[i].w, s)) << 16);
-                if (lane == 0) a.hs[r * a.hs_pitch + blk] = s;
+                if (lane == 0) a.hs[(first + j) * a.hs_pitch + blk] = s;
               }
             }
           }
@@ -867,13 +863,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
         uint8_t* hb = xh + h.i * a.hbuf_bytes;
         if (lane == 0) mbar_arrive_expect_tx(&sm->hfull[h.i], ntok * (a.I + a.hs_pitch * 4));
         __syncwarp();
-        for (int j = 0; j < ntok; ++j) {
-          const size_t row = sm->ent_row[first + j];
-          for (int k = lane; k < kb_i; k += 32)
-            bulk_load(hb + k * tile_bytes + j * 128, a.hq + row * a.I + k * 128, 128, &sm->hfull[h.i]);
-          if (lane == 31)
-            bulk_load(hb + kb_i * tile_bytes + j * a.hs_pitch * 4, a.hs + row * a.hs_pitch, a.hs_pitch * 4, &sm->hfull[h.i]);
-        }
+        for (int k = lane; k < kb_i; k += 32)
+          bulk_load(hb + k * tile_bytes, a.hq + static_cast<size_t>(first) * a.I + k * ntok * 128, ntok * 128, &sm->hfull[h.i]);
+        if (lane == 31)
+          bulk_load(hb + kb_i * tile_bytes, a.hs + first * a.hs_pitch, ntok * a.hs_pitch * 4, &sm->hfull[h.i]);
         h.next(a.hbufs);
       }
       for (int j = max(0, n - a.hbufs); j < n; ++j) mbar_wait(&sm->hfull[j % a.hbufs], (j / a.hbufs) & 1, abort);
