@@ -203,7 +203,8 @@ __host__ __device__ inline int range_begin(int i, int n, int parts) {
 // Affinities of EB experts with TB tokens, a block of 8 warps. The selection is
 // a border, so the logits are summed in FP64 (their products are exact) and the
 // affinity is rounded once: keys that differ in FP32 are never exchanged by the
-// sum's order. EB x TB keeps what the blocks read from L2 together small.
+// sum's order. The 2 x 4 sums of a thread leave it the registers to load all
+// its runs at once (4 x 8 sums took 16 us at 13 tokens and d = 2048, these 8).
 __device__ __forceinline__ void to_double8(const uint4 v, double (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -215,9 +216,9 @@ __device__ __forceinline__ void to_double8(const uint4 v, double (&f)[8]) {
 
 __device__ __forceinline__ void quantise_u(const Args& a, int block, int blocks);
 
-template <int EB, int TB>
+constexpr int EB = 2, TB = 4;
 __global__ void __launch_bounds__(256) few_route_kernel(const Args a) {
-  constexpr int M = EB * TB;                 // sums of a thread: 8 or 32
+  constexpr int M = EB * TB;                 // sums of a thread
   static_assert(M <= 32 && (M & (M - 1)) == 0, "the sums spread over a warp's lanes");
   __shared__ double dots[8][M];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -228,35 +229,31 @@ __global__ void __launch_bounds__(256) few_route_kernel(const Args a) {
   double acc[M];
 #pragma unroll
   for (int i = 0; i < M; ++i) acc[i] = 0.0;
-  constexpr int AHEAD = M <= 8 ? 4 : 1;      // few sums leave registers to load all four runs at once
-#pragma unroll 1
-  for (int r = 0; r < 4; r += AHEAD) {
-    uint4 we[AHEAD][EB], x[AHEAD][TB];
+  uint4 we[4][EB], x[4][TB];
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      const int v = tid + (r + i) * 256;
+  for (int i = 0; i < 4; ++i) {
+    const int v = tid + i * 256;
 #pragma unroll
-      for (int k = 0; k < EB; ++k)
-        we[i][k] = v < V && e0 + k < a.N_r ? __ldg(reinterpret_cast<const uint4*>(a.e + static_cast<size_t>(e0 + k) * a.d) + v) : zero;
+    for (int k = 0; k < EB; ++k)
+      we[i][k] = v < V && e0 + k < a.N_r ? __ldg(reinterpret_cast<const uint4*>(a.e + static_cast<size_t>(e0 + k) * a.d) + v) : zero;
 #pragma unroll
-      for (int t = 0; t < TB; ++t)
-        x[i][t] = v < V && t0 + t < a.T ? __ldg(reinterpret_cast<const uint4*>(a.u + static_cast<size_t>(t0 + t) * a.d) + v) : zero;
-    }
+    for (int t = 0; t < TB; ++t)
+      x[i][t] = v < V && t0 + t < a.T ? __ldg(reinterpret_cast<const uint4*>(a.u + static_cast<size_t>(t0 + t) * a.d) + v) : zero;
+  }
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      double w[EB][8], f[8];
+  for (int i = 0; i < 4; ++i) {
+    double w[EB][8], f[8];
 #pragma unroll
-      for (int k = 0; k < EB; ++k) to_double8(we[i][k], w[k]);
+    for (int k = 0; k < EB; ++k) to_double8(we[i][k], w[k]);
 #pragma unroll
-      for (int t = 0; t < TB; ++t)
-        if (t0 + t < a.T) {
-          to_double8(x[i][t], f);
+    for (int t = 0; t < TB; ++t)
+      if (t0 + t < a.T) {
+        to_double8(x[i][t], f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int k = 0; k < EB; ++k) acc[k * TB + t] = fma(f[j], w[k][j], acc[k * TB + t]);
-        }
-    }
+          for (int k = 0; k < EB; ++k) acc[k * TB + t] = fma(f[j], w[k][j], acc[k * TB + t]);
+      }
   }
   // M sums over 32 lanes: each step halves the values a lane still holds
   int o = 16;
@@ -1031,10 +1028,7 @@ extern "C" int moe_few_tokens(const uint16_t* u, const uint8_t* xq, const float*
     const int q = d / a.members, n = q + (q % 2 == i ? 0 : 1);
     if (int st = make_tmap_2d(&maps.down[i], w_down, U8, 1, slots * d, I, n > 0 ? n : 1, 128)) return st;
   }
-  if (T <= 4)
-    few_route_kernel<2, 4><<<dim3((N_r + 1) / 2, 1), 256, 0, s>>>(a);
-  else
-    few_route_kernel<4, 8><<<dim3((N_r + 3) / 4, (T + 7) / 8), 256, 0, s>>>(a);
+  few_route_kernel<<<dim3((N_r + EB - 1) / EB, (T + TB - 1) / TB), 256, 0, s>>>(a);
   if (int st = launch_status("few tokens: router launch")) return st;
   return T <= 8 ? launch<8>(maps, a, G, s) : launch<16>(maps, a, G, s);
 }

@@ -57,6 +57,18 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* red) {
   }
 }
 
+// Four E4M3 codes of fl32(t / s) from t and inv = fl32(1 / s). t inv is within
+// 2^-23 of the quotient, so where both ends of a 2^-22 bracket round to the
+// same codes those are the codes; false where a rounding border lies inside,
+// and the values have to be divided. (Dividing every value by IEEE rules costs
+// about half of a row's instructions.)
+__device__ __forceinline__ bool codes_by_reciprocal(const float* t, float inv, uint32_t& q) {
+  constexpr float LO = 1.0f - 0x1p-22f, HI = 1.0f + 0x1p-22f;
+  const float a = t[0] * inv, b = t[1] * inv, c = t[2] * inv, d = t[3] * inv;
+  q = e4m3x2(a * LO, b * LO) | (e4m3x2(c * LO, d * LO) << 16);
+  return q == (e4m3x2(a * HI, b * HI) | (e4m3x2(c * HI, d * HI) << 16));
+}
+
 // One row per blockDim.x threads, VPT runs of 8 channels a thread, held in
 // registers between the sum of squares and the outputs.
 template <typename S, typename W, int VPT>
@@ -108,11 +120,17 @@ __global__ void __launch_bounds__(1024) rmsnorm_quant_kernel(const uint16_t* x, 
       for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       if (on) {
         const float sc = tile_scale(amax);
+        const float inv = __frcp_rn(sc);
         uint32_t c[2];
+        bool sure = sc >= 0x1p-100f;         // 1 / sc and the products are normal numbers
+        sure = codes_by_reciprocal(t, inv, c[0]) && sure;
+        sure = codes_by_reciprocal(t + 4, inv, c[1]) && sure;
+        if (!sure) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          c[k] = e4m3x2(__fdiv_rn(t[4 * k], sc), __fdiv_rn(t[4 * k + 1], sc)) |
-                 (e4m3x2(__fdiv_rn(t[4 * k + 2], sc), __fdiv_rn(t[4 * k + 3], sc)) << 16);
+          for (int k = 0; k < 2; ++k)
+            c[k] = e4m3x2(__fdiv_rn(t[4 * k], sc), __fdiv_rn(t[4 * k + 1], sc)) |
+                   (e4m3x2(__fdiv_rn(t[4 * k + 2], sc), __fdiv_rn(t[4 * k + 3], sc)) << 16);
+        }
         *reinterpret_cast<uint2*>(q + base + v * 8) = make_uint2(c[0], c[1]);
         if ((v & 15) == 0) scale[static_cast<size_t>(row) * (d >> 7) + (v >> 4)] = sc;
       }
@@ -120,68 +138,145 @@ __global__ void __launch_bounds__(1024) rmsnorm_quant_kernel(const uint16_t* x, 
   }
 }
 
+// Sums two values over the `warps` warps of a block's rows; every thread gets
+// the sums. red: 64 floats, of a pair that the next call does not use.
+__device__ __forceinline__ void block_sum2(float& a, float& b, float* red, int warps) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  if (warps == 1) return;
+  const int warp = threadIdx.x >> 5, lane = lane_id();
+  if (lane == 0) { red[warp] = a; red[32 + warp] = b; }
+  named_bar_sync(1, warps * 32);
+  a = lane < warps ? red[lane] : 0.0f;
+  b = lane < warps ? red[32 + lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+}
+
+__device__ __forceinline__ void bulk_row(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+constexpr int MAX_RING = 8;
+
 // Rows blockIdx.x, blockIdx.x + gridDim.x, ..: a thread owns its channels for
-// all of them, so dw needs no exchange before the partial row it writes.
+// all of them, so w stays in registers and dw needs no exchange before the
+// partial row it writes. The last warp keeps a ring of whole rows (h, dy, dres)
+// on their way into shared memory by bulk copies: a row is used twice with a
+// sum over the block between, and with plain loads the block stood still for
+// their latency twice a row (T = 8192, d = 7168: 247 us).
 template <typename S, typename W, int VPT>
-__global__ void __launch_bounds__(512) rmsnorm_backward_kernel(const uint16_t* dy, const S* h, const W* w,
-                                                               float eps, const S* dres, int rows, int d, S* dh,
+__global__ void __launch_bounds__(544) rmsnorm_backward_kernel(const uint16_t* dy, const S* h, const W* w, float eps,
+                                                               const S* dres, int rows, int d, int ring, S* dh,
                                                                float* part) {
-  __shared__ float red_all[2][2 * 32];
-  const int V = d >> 3;
-  float dw[VPT][8];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
-  int flip = 0;
-  for (int row = blockIdx.x; row < rows; row += gridDim.x, flip ^= 1) {
-    const size_t base = static_cast<size_t>(row) * d;
-    float hv[VPT][8], gy[VPT][8];
-    float sum[2] = {0.0f, 0.0f};             // sum h^2, sum dy w h
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint64_t full[MAX_RING], empty[MAX_RING];
+  __shared__ float red_all[2][64];
+  __shared__ int abort_flag;
+  volatile int* abort = &abort_flag;
+  const int warps = (blockDim.x >> 5) - 1, warp = threadIdx.x >> 5;
+  const uint32_t hb = d * sizeof(S), yb = d * 2, stage = hb + yb + (dres != nullptr ? hb : 0);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ring; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], warps); }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (warp == warps) {
+    if (lane_id() == 0) {
+      int s = 0, n = 0;
+      uint32_t lap = 1;
+      bool ok = true;
+      // dh may lie over h or dres: a row is written only after its own copies have landed
+      for (int row = blockIdx.x; ok && row < rows; row += gridDim.x, ++n) {
+        if (!(ok = mbar_wait(&empty[s], lap, abort))) break;
+        uint8_t* dst = smem + static_cast<size_t>(s) * stage;
+        const size_t base = static_cast<size_t>(row) * d;
+        mbar_arrive_expect_tx(&full[s], stage);
+        bulk_row(dst, h + base, hb, &full[s]);
+        bulk_row(dst + hb, dy + base, yb, &full[s]);
+        if (dres != nullptr) bulk_row(dst + hb + yb, dres + base, hb, &full[s]);
+        if (++s == ring) { s = 0; lap ^= 1; }
+      }
+      for (int j = max(0, n - ring); j < n; ++j) mbar_wait(&full[j % ring], (j / ring) & 1, abort);
+    }
+  } else {
+    const int V = d >> 3;
+    float dw[VPT][8], wv[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v < V) {
-        float wv[8];
-        load8(h + base + v * 8, hv[i]);
-        load8(dy + base + v * 8, gy[i]);
-        load8(w + v * 8, wv);
+      const int v = threadIdx.x + i * warps * 32;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          sum[0] = fmaf(hv[i][j], hv[i][j], sum[0]);
-          sum[1] = fmaf(gy[i][j] * wv[j], hv[i][j], sum[1]);
+      for (int j = 0; j < 8; ++j) dw[i][j] = wv[i][j] = 0.0f;
+      if (v < V) load8(w + v * 8, wv[i]);
+    }
+    int s = 0, flip = 0;
+    uint32_t lap = 0;
+    bool ok = true;
+    for (int row = blockIdx.x; row < rows; row += gridDim.x, flip ^= 1) {
+      ok = ok && warp_wait(&full[s], lap, abort);
+      const uint8_t* src = smem + static_cast<size_t>(s) * stage;
+      float hv[VPT][8], gy[VPT][8];
+      float hh = 0.0f, gh = 0.0f;            // sum h^2, sum dy w h
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = threadIdx.x + i * warps * 32;
+        if (v < V) {
+          load8(reinterpret_cast<const S*>(src) + v * 8, hv[i]);
+          load8(reinterpret_cast<const uint16_t*>(src + hb) + v * 8, gy[i]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            hh = fmaf(hv[i][j], hv[i][j], hh);
+            gh = fmaf(gy[i][j] * wv[i][j], hv[i][j], gh);
+          }
         }
       }
+      block_sum2(hh, gh, red_all[flip], warps);
+      const float r = __frsqrt_rn(hh / static_cast<float>(d) + eps);
+      const float c = gh / static_cast<float>(d) * r * r;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = threadIdx.x + i * warps * 32;
+        if (v < V) {
+          float o[8];
+          if constexpr (VPT > 2) {           // too many to keep: read again
+            load8(reinterpret_cast<const S*>(src) + v * 8, hv[i]);
+            load8(reinterpret_cast<const uint16_t*>(src + hb) + v * 8, gy[i]);
+          }
+          if (dres != nullptr) {
+            load8(reinterpret_cast<const S*>(src + hb + yb) + v * 8, o);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = 0.0f;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            dw[i][j] = fmaf(gy[i][j], hv[i][j] * r, dw[i][j]);
+            o[j] = fmaf(r, gy[i][j] * wv[i][j] - hv[i][j] * c, o[j]);
+          }
+          if (ok) store8(dh + static_cast<size_t>(row) * d + v * 8, o);
+        }
+      }
+      __syncwarp();
+      if (lane_id() == 0) mbar_arrive(&empty[s]);
+      if (++s == ring) { s = 0; lap ^= 1; }
     }
-    row_sum(sum, red_all[flip]);             // two buffers: the next row's sums may start early
-    const float r = __frsqrt_rn(sum[0] / static_cast<float>(d) + eps);
-    const float c = sum[1] / static_cast<float>(d) * r * r;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v < V) {
-        float wv[8], o[8];
-        load8(w + v * 8, wv);
-        if (dres != nullptr) {
-          load8(dres + base + v * 8, o);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          dw[i][j] = fmaf(gy[i][j], hv[i][j] * r, dw[i][j]);
-          o[j] = fmaf(r, gy[i][j] * wv[j] - hv[i][j] * c, o[j]);
-        }
-        store8(dh + base + v * 8, o);
-      }
+      const int v = threadIdx.x + i * warps * 32;
+      if (v < V) store8(part + static_cast<size_t>(blockIdx.x) * d + v * 8, dw[i]);
     }
   }
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = threadIdx.x + i * blockDim.x;
-    if (v < V) store8(part + static_cast<size_t>(blockIdx.x) * d + v * 8, dw[i]);
-  }
+  __syncthreads();
 }
 
 // dw = sum of the n partial rows, in a fixed order: 32 columns a block, eight
@@ -277,18 +372,31 @@ extern "C" int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int strea
   DeviceInfo di;
   if (int st = device_info(&di)) return st;
   const int V = d / 8;
-  const int vpt = vpt_for(V, V > 256 * 4 || rows <= di.sm_count ? 512 : 256);
-  const int nt = ((V + vpt - 1) / vpt + 31) / 32 * 32;
-  int parts = di.sm_count * (nt <= 256 ? 3 : 2);
+  const int vpt = vpt_for(V, 512);
+  const int nt = ((V + vpt - 1) / vpt + 31) / 32 * 32 + 32;      // and the copying warp
+  const size_t row_bytes = static_cast<size_t>(d) * (2 + (stream_is_fp32 ? 4 : 2) * (dres ? 2 : 1));
+  int per_sm = nt <= 160 ? 4 : nt <= 288 ? 3 : row_bytes <= 36 * 1024 ? 2 : 1;
+  if (rows <= di.sm_count) per_sm = 1;
+  int ring = static_cast<int>(220 * 1024 / per_sm / row_bytes);
+  if (ring > MAX_RING) ring = MAX_RING;
+  if (ring < 1) ring = 1;
+  int parts = di.sm_count * per_sm;
   if (parts > rows) parts = rows;
   if (parts > MAX_PARTS) parts = MAX_PARTS;
+  const int most = (rows + parts - 1) / parts;                   // rows of a block
+  if (ring > most) ring = most;
+  const size_t smem = ring * row_bytes;
   float* part = parts == 1 ? dw : static_cast<float*>(workspace);
+  int attr = MOE_OK;
   auto launch = [&](auto s, auto wt, auto n) {
     using S = decltype(s);
     using W = decltype(wt);
-    rmsnorm_backward_kernel<S, W, decltype(n)::value><<<parts, nt, 0, st_>>>(
-        dy, static_cast<const S*>(h), static_cast<const W*>(w), eps, static_cast<const S*>(dres), rows, d,
-        static_cast<S*>(dh), part);
+    auto k = rmsnorm_backward_kernel<S, W, decltype(n)::value>;
+    attr = cuda_status(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)),
+                       "rmsnorm backward: smem attribute");
+    if (attr == MOE_OK)
+      k<<<parts, nt, smem, st_>>>(dy, static_cast<const S*>(h), static_cast<const W*>(w), eps, static_cast<const S*>(dres),
+                                  rows, d, ring, static_cast<S*>(dh), part);
   };
   auto by_vpt = [&](auto s, auto wt) {
     if (vpt == 1) launch(s, wt, std::integral_constant<int, 1>{});
@@ -297,6 +405,7 @@ extern "C" int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int strea
   };
   if (stream_is_fp32) { if (w_is_bf16) by_vpt(0.0f, uint16_t(0)); else by_vpt(0.0f, 0.0f); }
   else { if (w_is_bf16) by_vpt(uint16_t(0), uint16_t(0)); else by_vpt(uint16_t(0), 0.0f); }
+  if (attr != MOE_OK) return attr;
   if (int st = launch_status("rmsnorm backward launch")) return st;
   if (parts > 1) {
     column_sum_kernel<<<(d + 31) / 32, dim3(32, 8), 0, st_>>>(part, parts, d, dw);
