@@ -69,6 +69,33 @@ __device__ __forceinline__ bool codes_by_reciprocal(const float* t, float inv, u
   return q == (e4m3x2(a * HI, b * HI) | (e4m3x2(c * HI, d * HI) << 16));
 }
 
+// Eight values t of a 1x128 tile, held by 16 neighbouring lanes: their codes and
+// the tile's scale (moe_quant_1x128's rule). Every lane of the warp calls it;
+// `on` is the same for the 16 lanes of a tile.
+__device__ __forceinline__ void store_codes(const float (&t)[8], bool on, uint8_t* q, float* scale, bool first) {
+  float amax = 0.0f;
+  if (on)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(t[j]));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if (!on) return;
+  const float sc = tile_scale(amax);
+  const float inv = __frcp_rn(sc);
+  uint32_t c[2];
+  bool sure = sc >= 0x1p-100f;               // 1 / sc and the products are normal numbers
+  sure = codes_by_reciprocal(t, inv, c[0]) && sure;
+  sure = codes_by_reciprocal(t + 4, inv, c[1]) && sure;
+  if (!sure) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      c[k] = e4m3x2(__fdiv_rn(t[4 * k], sc), __fdiv_rn(t[4 * k + 1], sc)) |
+             (e4m3x2(__fdiv_rn(t[4 * k + 2], sc), __fdiv_rn(t[4 * k + 3], sc)) << 16);
+  }
+  *reinterpret_cast<uint2*>(q) = make_uint2(c[0], c[1]);
+  if (first) *scale = sc;
+}
+
 // One row per blockDim.x threads, VPT runs of 8 channels a thread, held in
 // registers between the sum of squares and the outputs.
 template <typename S, typename W, int VPT>
@@ -102,39 +129,17 @@ __global__ void __launch_bounds__(1024) rmsnorm_quant_kernel(const uint16_t* x, 
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
-    const bool on = live && v < V;           // uniform over the 16 lanes of a tile
+    const bool on = live && v < V;
     float t[8];
-    float amax = 0.0f;
     if (on) {
       if (h != nullptr) store8(h + base + v * 8, s[i]);
       load8(w + v * 8, t);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        t[j] *= s[i][j] * rstd;
-        amax = fmaxf(amax, fabsf(t[j]));
-      }
+      for (int j = 0; j < 8; ++j) t[j] *= s[i][j] * rstd;
       if (y != nullptr) store8(y + base + v * 8, t);
     }
-    if (q != nullptr) {                      // uniform: every lane takes part in the shuffles
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      if (on) {
-        const float sc = tile_scale(amax);
-        const float inv = __frcp_rn(sc);
-        uint32_t c[2];
-        bool sure = sc >= 0x1p-100f;         // 1 / sc and the products are normal numbers
-        sure = codes_by_reciprocal(t, inv, c[0]) && sure;
-        sure = codes_by_reciprocal(t + 4, inv, c[1]) && sure;
-        if (!sure) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            c[k] = e4m3x2(__fdiv_rn(t[4 * k], sc), __fdiv_rn(t[4 * k + 1], sc)) |
-                   (e4m3x2(__fdiv_rn(t[4 * k + 2], sc), __fdiv_rn(t[4 * k + 3], sc)) << 16);
-        }
-        *reinterpret_cast<uint2*>(q + base + v * 8) = make_uint2(c[0], c[1]);
-        if ((v & 15) == 0) scale[static_cast<size_t>(row) * (d >> 7) + (v >> 4)] = sc;
-      }
-    }
+    if (q != nullptr)
+      store_codes(t, on, q + base + v * 8, scale + static_cast<size_t>(row) * (d >> 7) + (v >> 4), (v & 15) == 0);
   }
 }
 
@@ -191,6 +196,7 @@ __global__ void __launch_bounds__(544) rmsnorm_backward_kernel(const uint16_t* d
     fence_mbar_init();
   }
   __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == warps) {
     if (lane_id() == 0) {
       int s = 0, n = 0;
@@ -279,21 +285,22 @@ __global__ void __launch_bounds__(544) rmsnorm_backward_kernel(const uint16_t* d
   __syncthreads();
 }
 
-// dw = sum of the n partial rows, in a fixed order: 32 columns a block, eight
+// dw = sum of the n partial rows, in a fixed order: 32 columns a block, 32
 // threads a column.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ part, int n, int d, float* dw) {
-  __shared__ float red[8][33];
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float* part, int n, int d, float* dw) {
+  __shared__ float red[32][33];
   const int col = blockIdx.x * 32 + threadIdx.x;
   float s = 0.0f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");     // launched before the partial rows are there
   if (col < d)
-    for (int i = threadIdx.y; i < n; i += 8) s += part[static_cast<size_t>(i) * d + col];
+#pragma unroll 4
+    for (int i = threadIdx.y; i < n; i += 32) s += part[static_cast<size_t>(i) * d + col];
   red[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
-  if (threadIdx.y == 0 && col < d) {
+  s = red[threadIdx.x][threadIdx.y];                     // a warp a column
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += red[k][threadIdx.x];
-    dw[col] = s;
-  }
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (threadIdx.x == 0 && blockIdx.x * 32 + threadIdx.y < d) dw[blockIdx.x * 32 + threadIdx.y] = s;
 }
 
 constexpr int MAX_D = 1024 * 8 * 4;
@@ -372,10 +379,10 @@ extern "C" int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int strea
   DeviceInfo di;
   if (int st = device_info(&di)) return st;
   const int V = d / 8;
-  const int vpt = vpt_for(V, 512);
+  const int vpt = vpt_for(V, V <= 1024 ? 256 : 512);
   const int nt = ((V + vpt - 1) / vpt + 31) / 32 * 32 + 32;      // and the copying warp
   const size_t row_bytes = static_cast<size_t>(d) * (2 + (stream_is_fp32 ? 4 : 2) * (dres ? 2 : 1));
-  int per_sm = nt <= 160 ? 4 : nt <= 288 ? 3 : row_bytes <= 36 * 1024 ? 2 : 1;
+  int per_sm = nt <= 160 ? 4 : nt <= 288 && row_bytes <= 36 * 1024 ? 3 : row_bytes <= 54 * 1024 ? 2 : 1;
   if (rows <= di.sm_count) per_sm = 1;
   int ring = static_cast<int>(220 * 1024 / per_sm / row_bytes);
   if (ring > MAX_RING) ring = MAX_RING;
@@ -408,8 +415,17 @@ extern "C" int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int strea
   if (attr != MOE_OK) return attr;
   if (int st = launch_status("rmsnorm backward launch")) return st;
   if (parts > 1) {
-    column_sum_kernel<<<(d + 31) / 32, dim3(32, 8), 0, st_>>>(part, parts, d, dw);
-    return launch_status("rmsnorm backward: column sums");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((d + 31) / 32);
+    cfg.blockDim = dim3(32, 32);
+    cfg.stream = st_;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, column_sum_kernel, static_cast<const float*>(part), parts, d, dw),
+                       "rmsnorm backward: column sums");
   }
   return MOE_OK;
 }
