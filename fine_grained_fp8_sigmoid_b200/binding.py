@@ -407,41 +407,56 @@ def moe_bias_update(b, counts, T, K_r, gamma=0.001, max_over_mean=None, stream=N
         _stream(stream)))
 
 
-def _one_device(*tensors):
-    """All tensors live on the current device (kernels launch there)."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
+# The calls below are short (a few microseconds on the device), so their checks
+# are one expression a tensor; what fails it is named by the slow ones above.
+
+def _here(stream):
+    """The current device, and the stream's handle (the current stream's by default)."""
+    dev = torch.cuda.current_device()
+    return dev, (torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
 
 
-def _stream_type(t, name):
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"{name} must be bf16 or FP32")
-    return t.dtype
+def _p(t, dtype, shape, dev, name):
+    """The address of a checked tensor: dtype, shape, contiguous, on device dev."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _want(t, dtype, shape, name)
+    raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+
+
+def _popt(t, dtype, shape, dev, name):
+    return None if t is None else _p(t, dtype, shape, dev, name)
+
+
+def _ws(t, dev):
+    """(address, bytes) of a workspace."""
+    if t is None or not t.is_cuda or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{dev}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
 
 
 def moe_rmsnorm_quant(x, w, eps, y=None, q=None, scale=None, residual=None, h=None, stream=None):
     """s = x + residual; h = s; y = s / sqrt(mean(s^2) + eps) * w in bf16 and,
     as q and scale, in E4M3 1x128 tiles. x may be a column slice of a wider
     row-major tensor; residual and h are bf16 or FP32, w FP32 or bf16; outputs
-    that are None are not written."""
+    that are None are not written. h may be residual, y may be x."""
     ld = _ld(x)
     rows, d = x.shape
-    if x.dtype != torch.bfloat16:
-        raise ValueError("x must be bf16")
-    st = torch.bfloat16 if residual is None and h is None else _stream_type(residual if residual is not None else h,
-                                                                            "the stream")
-    _opt(residual, st, (rows, d), "residual")
-    _opt(h, st, (rows, d), "h")
-    _want(w, _stream_type(w, "w"), (d,), "w")
-    _opt(y, torch.bfloat16, (rows, d), "y")
-    _opt(q, torch.uint8, (rows, d), "q")
-    _opt(scale, torch.float32, (rows, d // 128), "scale")
-    _one_device(x, w, residual, h, y, q, scale)
+    dev, handle = _here(stream)
+    if x.dtype is not torch.bfloat16 or x.get_device() != dev:
+        raise ValueError(f"x must be bf16 on cuda:{dev}")
+    st = residual.dtype if residual is not None else h.dtype if h is not None else torch.bfloat16
+    if st not in _FLOATS or w.dtype not in _FLOATS:
+        raise ValueError("residual, h and w must be bf16 or FP32")
+    bf, rd = torch.bfloat16, (rows, d)
     check("moe_rmsnorm_quant", _lib.load().moe_rmsnorm_quant(
-        _ptr(x), ld if rows > 1 else d, _ptr(residual), int(st == torch.float32), _ptr(w), int(w.dtype == torch.bfloat16), eps, rows, d,
-        _ptr(h), _ptr(y), _ptr(q), _ptr(scale), _stream(stream)))
+        x.data_ptr(), ld if rows > 1 else d, _popt(residual, st, rd, dev, "residual"), st is torch.float32,
+        _p(w, w.dtype, (d,), dev, "w"), w.dtype is bf, eps, rows, d, _popt(h, st, rd, dev, "h"),
+        _popt(y, bf, rd, dev, "y"), _popt(q, torch.uint8, rd, dev, "q"),
+        _popt(scale, torch.float32, (rows, d // 128), dev, "scale"), handle))
 
 
 def moe_rmsnorm_backward_workspace(rows, d):
@@ -450,19 +465,18 @@ def moe_rmsnorm_backward_workspace(rows, d):
 
 def moe_rmsnorm_backward(dy, h, w, eps, dh, dw, workspace, dres=None, stream=None):
     """dh = dres + d(norm of h)/dh . dy and dw [d] FP32; h, dres and dh share
-    one type (bf16 or FP32), dy is bf16, w FP32 or bf16."""
+    one type (bf16 or FP32), dy is bf16, w FP32 or bf16. dh may be h or dres."""
     rows, d = h.shape
-    st = _stream_type(h, "h")
-    _want(dy, torch.bfloat16, (rows, d), "dy")
-    _want(h, st, (rows, d), "h")
-    _want(w, _stream_type(w, "w"), (d,), "w")
-    _opt(dres, st, (rows, d), "dres")
-    _want(dh, st, (rows, d), "dh")
-    _want(dw, torch.float32, (d,), "dw")
-    _one_device(dy, h, w, dres, dh, dw, workspace)
+    dev, handle = _here(stream)
+    st = h.dtype
+    if st not in _FLOATS or w.dtype not in _FLOATS:
+        raise ValueError("h and w must be bf16 or FP32")
+    rd = (rows, d)
+    ws, ws_bytes = _ws(workspace, dev)
     check("moe_rmsnorm_backward", _lib.load().moe_rmsnorm_backward(
-        _ptr(dy), _ptr(h), int(st == torch.float32), _ptr(w), int(w.dtype == torch.bfloat16), eps, _ptr(dres), rows, d,
-        _ptr(dh), _ptr(dw), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+        _p(dy, torch.bfloat16, rd, dev, "dy"), _p(h, st, rd, dev, "h"), st is torch.float32,
+        _p(w, w.dtype, (d,), dev, "w"), w.dtype is torch.bfloat16, eps, _popt(dres, st, rd, dev, "dres"), rows, d,
+        _p(dh, st, rd, dev, "dh"), _p(dw, torch.float32, (d,), dev, "dw"), ws, ws_bytes, handle))
 
 
 def moe_few_tokens_workspace(T, d, N_r, K_r, I):
@@ -471,34 +485,24 @@ def moe_few_tokens_workspace(T, d, N_r, K_r, I):
 
 def moe_few_tokens(u, e, b, K_r, w_gate, w_up, w_down, s_gate, s_up, s_down, out, topk_idx, gates, workspace,
                    xq=None, xs=None, base=None, counts=None, stream=None):
-    """The whole layer for at most 16 tokens in one kernel: routes u, runs the
+    """The whole layer for at most 16 tokens in two kernels: routes u, runs the
     selected experts and the shared one on xq/xs (u quantised inside when they
     are None), and writes base (u when None) plus their gated sum to out."""
     T, d = u.shape
     N_r = b.shape[0]
-    I = w_gate.shape[1]
-    _want(u, torch.bfloat16, (T, d), "u")
-    _want(e, torch.bfloat16, (N_r, d), "e")
-    _want(b, torch.float32, (N_r,), "b")
-    _want(w_gate, torch.uint8, (N_r + 1, I, d), "w_gate")
-    _want(w_up, torch.uint8, (N_r + 1, I, d), "w_up")
-    _want(w_down, torch.uint8, (N_r + 1, d, I), "w_down")
-    _want(s_gate, torch.float32, (N_r + 1, I // 128, d // 128), "s_gate")
-    _want(s_up, torch.float32, (N_r + 1, I // 128, d // 128), "s_up")
-    _want(s_down, torch.float32, (N_r + 1, d // 128, I // 128), "s_down")
-    _want(out, torch.bfloat16, (T, d), "out")
-    _want(topk_idx, torch.int32, (T, K_r), "topk_idx")
-    _want(gates, torch.float32, (T, K_r), "gates")
-    _opt(xq, torch.uint8, (T, d), "xq")
-    _opt(xs, torch.float32, (T, d // 128), "xs")
-    _opt(base, torch.bfloat16, (T, d), "base")
-    _opt(counts, torch.int32, (N_r,), "counts")
-    _one_device(u, e, b, w_gate, w_up, w_down, s_gate, s_up, s_down, out, topk_idx, gates, workspace, xq, xs, base,
-                counts)
+    G, I = N_r + 1, w_gate.shape[1]
+    dev, handle = _here(stream)
+    bf, f32, u8, i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+    td, tk, wi, si = (T, d), (T, K_r), (G, I, d), (G, I // 128, d // 128)
+    ws, ws_bytes = _ws(workspace, dev)
     check("moe_few_tokens", _lib.load().moe_few_tokens(
-        _ptr(u), _ptr(xq), _ptr(xs), _ptr(base), _ptr(e), _ptr(b), T, d, N_r, K_r, _ptr(w_gate), _ptr(w_up),
-        _ptr(w_down), _ptr(s_gate), _ptr(s_up), _ptr(s_down), I, _ptr(out), _ptr(topk_idx), _ptr(gates),
-        _ptr(counts), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+        _p(u, bf, td, dev, "u"), _popt(xq, u8, td, dev, "xq"), _popt(xs, f32, (T, d // 128), dev, "xs"),
+        _popt(base, bf, td, dev, "base"), _p(e, bf, (N_r, d), dev, "e"), _p(b, f32, (N_r,), dev, "b"), T, d, N_r, K_r,
+        _p(w_gate, u8, wi, dev, "w_gate"), _p(w_up, u8, wi, dev, "w_up"), _p(w_down, u8, (G, d, I), dev, "w_down"),
+        _p(s_gate, f32, si, dev, "s_gate"), _p(s_up, f32, si, dev, "s_up"),
+        _p(s_down, f32, (G, d // 128, I // 128), dev, "s_down"), I, _p(out, bf, td, dev, "out"),
+        _p(topk_idx, i32, tk, dev, "topk_idx"), _p(gates, f32, tk, dev, "gates"),
+        _popt(counts, i32, (N_r,), dev, "counts"), ws, ws_bytes, handle))
 
 
 def moe_debug_wait_timeout(timeout_us, stream=None):

@@ -379,7 +379,9 @@ extern "C" int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int strea
   DeviceInfo di;
   if (int st = device_info(&di)) return st;
   const int V = d / 8;
-  const int vpt = vpt_for(V, V <= 1024 ? 256 : 512);
+  // Threads a row, measured at 8192 rows: 256 channels of 8 take 36 us with 128 threads and four blocks an SM, 39
+  // with 256 and three; 896 take 82 us with 224 threads and two blocks, 107 with 448 and one.
+  const int vpt = vpt_for(V, V <= 256 ? 128 : V <= 1024 ? 256 : 512);
   const int nt = ((V + vpt - 1) / vpt + 31) / 32 * 32 + 32;      // and the copying warp
   const size_t row_bytes = static_cast<size_t>(d) * (2 + (stream_is_fp32 ? 4 : 2) * (dres ? 2 : 1));
   int per_sm = nt <= 160 ? 4 : nt <= 288 && row_bytes <= 36 * 1024 ? 3 : row_bytes <= 54 * 1024 ? 2 : 1;

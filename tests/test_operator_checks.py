@@ -100,16 +100,38 @@ def test_few_tokens_refusals():
     assert lib.moe_few_tokens_workspace(4, 256, 8, 9, 128) == 0
 
 
-def test_binding_refuses_host_tensors():
+class _OnDevice:
+    """A host tensor that says it lives on CUDA device `dev`."""
+
+    def __init__(self, t, dev):
+        self._t, self._dev, self.is_cuda, self.device = t, dev, True, f"cuda:{dev}"
+
+    def get_device(self):
+        return self._dev
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+
+def test_binding_names_what_is_wrong():
     bf = torch.bfloat16
-    x, w = torch.zeros(4, 128, dtype=bf), torch.ones(128)
-    with pytest.raises(ValueError, match="CUDA"):
-        B.moe_rmsnorm_quant(x, w, 1e-6, y=torch.empty_like(x))
-    with pytest.raises(ValueError, match="CUDA"):
-        B.moe_rmsnorm_backward(x, x, w, 1e-6, x, w, torch.empty(4096, dtype=torch.uint8))
-    z8, zf = torch.zeros(3, 128, 256, dtype=torch.uint8), torch.zeros(3, 1, 2)
-    u = torch.zeros(4, 256, dtype=bf)
-    with pytest.raises(ValueError, match="CUDA"):
-        B.moe_few_tokens(u, torch.zeros(2, 256, dtype=bf), torch.zeros(2), 1, z8, z8, z8.view(3, 256, 128), zf, zf,
-                         zf.view(3, 2, 1), u, torch.zeros(4, 1, dtype=torch.int32), torch.zeros(4, 1),
-                         torch.empty(1 << 20, dtype=torch.uint8))
+    x = torch.zeros(4, 128, dtype=bf)
+    with pytest.raises(ValueError, match="y must be a CUDA tensor"):
+        B._p(x, bf, (4, 128), 0, "y")
+    with pytest.raises(ValueError, match="y: dtype"):
+        B._p(_OnDevice(x, 0), torch.float32, (4, 128), 0, "y")
+    with pytest.raises(ValueError, match="y: shape"):
+        B._p(_OnDevice(x, 0), bf, (4, 256), 0, "y")
+    with pytest.raises(ValueError, match="y must be contiguous"):
+        B._p(_OnDevice(x.t(), 0), bf, (128, 4), 0, "y")
+    with pytest.raises(ValueError, match="y is on cuda:1, but the current device is cuda:0"):
+        B._p(_OnDevice(x, 1), bf, (4, 128), 0, "y")
+    with pytest.raises(ValueError, match="y is required"):
+        B._p(None, bf, (4, 128), 0, "y")
+    assert B._p(_OnDevice(x, 0), bf, (4, 128), 0, "y") == x.data_ptr()
+    assert B._popt(None, bf, (4, 128), 0, "y") is None
+    for bad in (None, x, _OnDevice(x, 1), _OnDevice(x.t(), 0)):
+        with pytest.raises(ValueError, match="workspace"):
+            B._ws(bad, 0)
+    with pytest.raises(ValueError, match="CUDA matrix"):
+        B.moe_rmsnorm_quant(x, torch.ones(128), 1e-6, y=x)
