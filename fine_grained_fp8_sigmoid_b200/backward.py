@@ -96,6 +96,21 @@ class ExpertFFNBackward:
             out.update(self._wgrad(dy, dgu, xq, xs))
         return out
 
+    def norm_backward(self, du, norm_w, eps=1e-6, dres=None):
+        """The gradient of forward_prenorm's norm: du [T][d] bf16 is the whole
+        gradient of u (backward()'s dx and the router's share), dres what
+        reaches the stream h past the norm (the gradient of the layer's
+        output). Returns dict(dh [T][d] bf16, the gradient of x and residual
+        alike, and dw [d] FP32); reads the layer's h of that forward."""
+        L = self.layer
+        if L.h is None:
+            raise ValueError("norm_backward needs MoELayerFP8(prenorm=True)")
+        dh = torch.empty_like(L.h)
+        dw = torch.empty(L.d, dtype=torch.float32, device=L.device)
+        ws = torch.empty(B.moe_rmsnorm_backward_workspace(L.T, L.d), dtype=torch.uint8, device=L.device)
+        B.moe_rmsnorm_backward(du, L.h, norm_w, eps, dh, dw, ws, dres=dres)
+        return dict(dh=dh, dw=dw)
+
     def _wgrad(self, dy, dgu, xq, xs):
         L = self.layer
         T, d, I, N = L.T, L.d, L.I, L.N_r

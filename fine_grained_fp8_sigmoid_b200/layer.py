@@ -31,10 +31,19 @@ class MoELayerFP8:
     default) runs moe_route and moe_quant_1x128 apart. Both give the same
     codes and scales bit for bit. Measured at prefill: 169 us fused against
     65 + 53 us apart; the quantisation's 7168 IEEE divisions per token then
-    run on the router's eight epilogue warps per SM instead of a full grid."""
+    run on the router's eight epilogue warps per SM instead of a full grid.
+
+    few=True (T <= 16) runs forward as moe_few_tokens: the whole layer in two
+    kernels, each touched expert's weights read once, expert outputs summed in
+    FP32 (the separate steps round them to bf16 first).
+
+    prenorm=True adds the buffers of forward_prenorm: h, the residual stream
+    after the addition, and u, its root-mean-square norm."""
 
     def __init__(self, T: int, d: int, N_r: int, K_r: int, I: int, device="cuda", gather=None,
-                 fuse_quant=False):
+                 fuse_quant=False, few=False, prenorm=False):
+        if few and T > 16:
+            raise ValueError("few=True is for at most 16 tokens")
         self.T, self.d, self.N_r, self.K_r, self.I = T, d, N_r, K_r, I
         self.fuse_quant = bool(fuse_quant)
         self.gather = (T * K_r <= 64 * N_r) if gather is None else bool(gather)
@@ -67,6 +76,11 @@ class MoELayerFP8:
         self.ws_perm = torch.empty(max(B.moe_permute_workspace(T, N_r), 16), dtype=u8, **dev)
         self.ws_gemm = torch.empty(max(B.moe_grouped_gemm_fp8_workspace(T, K_r, d, I), 256),
                                    dtype=u8, **dev)
+        self.few = bool(few)
+        self.ws_few = (torch.empty(B.moe_few_tokens_workspace(T, d, N_r, K_r, I), dtype=u8, **dev)
+                       if few else None)
+        self.h = torch.empty(T, d, dtype=bf, **dev) if prenorm else None
+        self.u = torch.empty(T, d, dtype=bf, **dev) if prenorm else None
 
     def intermediate(self):
         """Views of the last step's expert intermediate H in the GEMM
@@ -125,7 +139,9 @@ class MoELayerFP8:
     def launches_per_step(self, update_bias=True):
         """Kernel launches of one forward: router (with the quantisation
         fused, or apart), permute (count, scan, scatter, and gather unless
-        fused), the GEMM's, combine, bias."""
+        fused), the GEMM's, combine, bias; with few, its two and bias."""
+        if self.few:
+            return 2 + int(update_bias)
         return ((1 if self.fuse_quant else 2) + (3 if self.gather else 4)
                 + B.moe_grouped_gemm_fp8_launches(self.d, self.I) + 1 + int(update_bias))
 
@@ -135,8 +151,41 @@ class MoELayerFP8:
     def bias_update(self, b, gamma=0.001, stream=None):
         B.moe_bias_update(b, self.counts, self.T, self.K_r, gamma, self.max_over_mean, stream)
 
+    def few_tokens(self, u, e, b, xq=None, xs=None, base=None, stream=None):
+        """The layer on few tokens; xq, xs: u's codes and scales if it has them."""
+        B.moe_few_tokens(u, e, b, self.K_r, self.w_gate, self.w_up, self.w_down, self.s_gate, self.s_up,
+                         self.s_down, self.out, self.topk_idx, self.gates, self.ws_few, xq=xq, xs=xs,
+                         base=base, counts=self.counts, stream=stream)
+
+    def forward_prenorm(self, x, norm_w, e, b, residual=None, eps=1e-6, update_bias=True, stream=None):
+        """The layer behind its pre-norm: h = x + residual (x without one),
+        u = h / sqrt(mean(h^2) + eps) * norm_w, returns self.out = h + shared +
+        gated experts of u. moe_rmsnorm_quant writes self.h, self.u and the
+        experts' xq, xs in one pass (xq quantises the FP32 norm, not the bf16
+        u). x and residual are bf16; residual may be self.out of the layer
+        before."""
+        if self.h is None:
+            raise ValueError("forward_prenorm needs MoELayerFP8(prenorm=True)")
+        B.moe_rmsnorm_quant(x, norm_w, eps, y=self.u, q=self.xq, scale=self.xs, residual=residual, h=self.h,
+                            stream=stream)
+        if self.few:
+            self.few_tokens(self.u, e, b, self.xq, self.xs, self.h, stream)
+        else:
+            B.moe_route(self.u, e, b, self.K_r, self.topk_idx, self.gates, stream=stream)
+            self.permute(stream)
+            self.experts(stream)
+            self.combine(self.h, stream)
+        if update_bias:
+            self.bias_update(b, stream=stream)
+        return self.out
+
     def forward(self, u, e, b, update_bias=True, stream=None):
         """One pass of the layer on device tensors; returns self.out."""
+        if self.few:
+            self.few_tokens(u, e, b, stream=stream)
+            if update_bias:
+                self.bias_update(b, stream=stream)
+            return self.out
         self.route(u, e, b, stream=stream)
         self.quant(u, stream)
         self.permute(stream)
