@@ -165,9 +165,16 @@ __device__ __forceinline__ void tmem_ld_async(uint32_t taddr, uint32_t* r) {
 
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
+// Counts up after everything the warp wrote before its last __syncwarp.
 __device__ __forceinline__ void count_up(unsigned* ctr) {
-  __threadfence();
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(ctr) : "memory");
+}
+
+// The same, acquiring what the others wrote before theirs; returns the count before.
+__device__ __forceinline__ int count_up_seen(int* ctr) {
+  int v;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(v) : "l"(ctr) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ unsigned count_now(const unsigned* ctr) {
@@ -768,12 +775,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
           else a.part[static_cast<size_t>(group) * a.T * a.d + at] = v;
         }
       if (a.groups > 1 && nrows > 0) {
-        __threadfence();
         named_bar_sync(3, PW * 32);
-        if (tid == 0) sm->last = atomicAdd(a.join_ctr + member, 1) == a.groups - 1;
+        if (tid == 0) sm->last = count_up_seen(a.join_ctr + member) == a.groups - 1;
         named_bar_sync(3, PW * 32);
         if (sm->last && r < nrows) {
-          __threadfence();
           for (int c = kq; c < a.T; c += SK) {
             const size_t at = static_cast<size_t>(c) * a.d + row0 + r;
             float v = bf16_bits_to_float(base[at]);
@@ -802,13 +807,11 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->redempty[buf]);
         // the warp that finishes a 128-block last quantises it
-        __threadfence();
-        __syncwarp();
         int last = 0;
         const int blk = ch >> 7;
-        if (lane == 0) last = atomicAdd(a.blk_ctr + slot * kb_i + blk, 1) == 128 / CH - 1;
+        if (lane == 0) last = count_up_seen(a.blk_ctr + slot * kb_i + blk) == 128 / CH - 1;
+        __syncwarp();
         if (__shfl_sync(0xffffffffu, last, 0)) {
-          __threadfence();
           for (int j0 = 0; j0 < ntok; j0 += 4) {         // four rows' loads in flight
             float4 x[4];
 #pragma unroll
@@ -831,7 +834,6 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
             }
           }
           fence_proxy_async_all();              // the codes are read by bulk copies
-          __threadfence();
           __syncwarp();
           if (lane == 0) count_up(a.slot_done + slot);
         }
@@ -853,7 +855,6 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
           const uint32_t missing = ~__ballot_sync(0xffffffffu, there);
           done = n + (missing ? __ffs(missing) - 1 : 32);
           __syncwarp();
-          __threadfence();
           fence_proxy_async_all();
         }
         const int first = sm->slot_start[si], ntok = sm->slot_start[si + 1] - first;
