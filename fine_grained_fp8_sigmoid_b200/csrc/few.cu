@@ -56,6 +56,7 @@ constexpr int SMEM_MAX = 227 * 1024;
 struct Maps {
   CUtensorMap gate, up;                      // CH rows, SK blocks: stored [block][row][128]
   CUtensorMap down[2];                       // a CTA's rows of W_down, by the parity of their count
+  CUtensorMap x;                             // the tokens' codes: every row, one block
 };
 
 struct Args {
@@ -130,6 +131,10 @@ struct Cursor {
     }
   }
 };
+
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile(
@@ -449,24 +454,6 @@ __device__ __forceinline__ void unit_at(const Args& a, int unit, int& slot, int&
   ch = (unit - slot * per) * CH;
 }
 
-// The tokens' codes as operand tiles [d/128][R][128], 128-byte swizzle
-// (rows behind T stay unset), and their scales [d/128][16].
-template <int R>
-__device__ __forceinline__ void stage_tokens(const Args& a, uint8_t* xh, float* xs) {
-  const int V = a.d >> 4, n = a.T * V;
-#pragma unroll 4
-  for (int o = threadIdx.x; o < n; o += CW * 32) {
-    const int t = o / V, v = o - t * V;
-    *reinterpret_cast<uint4*>(xh + (v >> 3) * (R * 128) + t * 128 + (((v & 7) ^ (t & 7)) << 4)) =
-        __ldcg(reinterpret_cast<const uint4*>(a.xq) + o);
-  }
-  const int kb_d = a.d >> 7;
-  for (int i = threadIdx.x; i < kb_d * COLS; i += CW * 32) {
-    const int t = i & (COLS - 1);
-    xs[i] = t < a.T ? __ldcg(a.xs + t * kb_d + (i >> 4)) : 0.0f;
-  }
-}
-
 // ---------------------------------------------------------------- kernel
 
 template <int R>
@@ -492,7 +479,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
     for (int i = 0; i < BUFS; ++i) { mbar_init(&sm->tfull[i], 1); mbar_init(&sm->tempty[i], PW); }
     for (int i = 0; i < EW; ++i) { mbar_init(&sm->redfull[i], PW); mbar_init(&sm->redempty[i], 1); }
     mbar_init(&sm->sel_ready, 1);
-    mbar_init(&sm->x_ready, 1);
+    mbar_init(&sm->x_ready, MI);
     mbar_init(&sm->x_free, MI);
     mbar_init(&sm->drained, MI);
     sm->abort = 0;
@@ -573,7 +560,20 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
     }
   } else if (warp >= CW + MI) {
     // ------------------------------------------------------------ MMA issuers (the whole warp keeps step)
-    bool ok = warp_wait(&sm->x_ready, 0, abort);
+    // the tokens' codes as operand tiles [d/128][R][128] (rows behind T stay unset), their scales as [d/128][16]
+    if (warp == CW + MI) {
+      if (lane == 0) mbar_expect_tx(&sm->x_ready, a.T * a.d);
+      __syncwarp();
+      for (int k = lane; k < kb_d; k += 32) tma_load_2d(xh + k * tile_bytes, &maps.x, &sm->x_ready, k * 128, 0);
+    }
+#pragma unroll 4
+    for (int i = (warp - CW - MI) * 32 + lane; i < kb_d * COLS; i += MI * 32) {
+      const int t = i & (COLS - 1);
+      xs[i] = t < a.T ? __ldg(a.xs + t * kb_d + (i >> 4)) : 0.0f;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm->x_ready);
+    bool ok = warp_wait(&sm->x_ready, 0, abort) && warp_wait(&sm->sel_ready, 0, abort);
     Cursor c, t;
     t.lap = 1;
     int turn = warp - CW - MI;                  // stages until this warp's next one
@@ -623,20 +623,17 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------ selection and the tokens' operand
+    // ------------------------------------------------------------ selection
     const int tid = threadIdx.x;
     select_all(a, sm, red);
-    stage_tokens<R>(a, xh, xs);
-    fence_proxy_async_smem();
     named_bar_sync(1, CW * 32);
-    if (tid == 0) mbar_arrive(&sm->x_ready);
     const int slots = sm->n_slots, units = slots * per;
 
     if (warp < PW) {
       // ---------------------------------------------------------- sums of the partials: a thread owns a TMEM lane
       // first phase: lanes are 32 gate rows of block 0, of block 1, 32 up rows of block 0, of block 1;
       // second phase: 64 rows of W_down in block 0, then in block 1
-      bool ok = true;
+      bool ok = warp_wait(&sm->x_ready, 0, abort);              // the scales
       Cursor t, e;
       e.lap = 1;
       int fin = 0;                              // the finishing warp of the unit at hand
@@ -1025,6 +1022,7 @@ extern "C" int moe_few_tokens(const uint16_t* u, const uint8_t* xq, const float*
   const uint64_t slots = static_cast<uint64_t>(N_r) + 1;
   if (int st = make_map(&maps.gate, w_gate, slots * I, d)) return st;
   if (int st = make_map(&maps.up, w_up, slots * I, d)) return st;
+  if (int st = make_tmap_2d(&maps.x, a.xq, U8, 1, T, d, T, 128)) return st;
   for (int i = 0; i < 2; ++i) {          // members own d / members rows or one more: one count is even, one odd
     const int q = d / a.members, n = q + (q % 2 == i ? 0 : 1);
     if (int st = make_tmap_2d(&maps.down[i], w_down, U8, 1, slots * d, I, n > 0 ? n : 1, 128)) return st;
