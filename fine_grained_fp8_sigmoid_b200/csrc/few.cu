@@ -4,23 +4,34 @@
 //
 // Every byte of the touched experts' weights is read once and nothing else is
 // large, so the second kernel is a stream of weights: one CTA per SM (a
-// cooperative launch), a producer that keeps a ring of TMA boxes in flight
-// across its phases, and the tensor cores behind it. The weights do not depend
-// on what the phases exchange, only on the selection, so the ring fills with
-// the shared expert during the selection and with W_down while the last
-// intermediate rows are written.
+// cooperative launch), producers that keep a ring of TMA boxes in flight across
+// its phases, and the tensor cores behind it. The weights do not depend on what
+// the phases exchange, only on the selection, so the ring fills with the shared
+// expert during the selection and with W_down while the last intermediate rows
+// are written. The first phase (gate, up, SwiGLU) is dealt in slot order and a
+// slot's second phase starts when its own intermediate is quantised, so the
+// phases need no barrier over the grid.
 //
 // Products: weight rows are the MMA's M side, tokens its N side. A stage of the
 // ring holds two 128-channel blocks of 64 weight rows, and one MMA takes both:
 // its 128 rows are the 64 rows of either block, its columns the R token rows
 // (8 or 16) of either block's activations, and of the four quarters of the
 // result the two that pair a block with itself are read. That keeps every
-// weight row live and halves the number of MMAs, whose issue (about 70 cycles
-// each, whatever their shape) would otherwise pace the kernel: 8 KB of weights
-// arrive in about 340 cycles. 64 rows is a choice of balance: one token has 9
+// weight row live and halves the number of MMAs, whose issue (70 to 100 cycles
+// each at these shapes, measured) otherwise paces the kernel: 8 KB of weights
+// arrive in about 340 cycles. For the same reason two warps issue MMAs and two
+// issue loads, in turns. 64 rows is a choice of balance: one token has 9
 // experts, 576 units of 32 gate and 32 up rows for 148 SMs (0.97 of them busy
-// in the last round), and in the second phase every CTA has its own d / SMs
-// rows of W_down, at most 64, over all slots.
+// in the last round), and in the second phase a CTA has its own d / SMs rows of
+// W_down, at most 64, over all slots.
+//
+// Measured back to back (d = 7168, I = 2048, 8 of 256 experts and the shared
+// one; weights alone take 61 / 216 / 704 us at the copy rate of 6.45 TB/s): one
+// token 75 us, of them 4 for the first kernel; 4 tokens 234 to 242 us; 16
+// tokens 713 to 790 us. DRAM bounds them; at one token the starts of the two
+// kernels and the selection (about 13 us) come on top. With small experts
+// (d = 2048, I = 1024, 6 of 64) one token takes 25 us against 7: the exchange
+// between the phases is six round trips through a loaded L2.
 #include "host.cuh"
 
 namespace moe {
@@ -33,7 +44,7 @@ constexpr int MAX_SLOTS = MAX_N + 1;
 constexpr int MAX_ENTRIES = MAX_T * MAX_K + MAX_T;
 constexpr int MAX_D = 8192;
 constexpr int CW = 8;                        // warps of the selection
-constexpr int EW = 3;                    // of them, finishing warps of the first phase
+constexpr int EW = 3;                        // of them, finishing warps of the first phase
 constexpr int PW = 4;                        // of them, warps that add up partials, one per 32 TMEM lanes
 constexpr int MI = 2;                        // producers, and MMA issuers: each kind takes turns, and the stages and
                                              // TMEM buffers are multiples of it
@@ -52,7 +63,7 @@ constexpr int MAX_GROUPS = 8;
 constexpr int MAX_MEMBERS = 256;             // and CTAs
 constexpr int SMEM_MAX = 227 * 1024;
 
-// Maps of the weights, rows [slot * rows] of codes, boxes of 128 channels by:
+// Tensor maps, all with the 128-byte swizzle. Weights are rows [slot * rows] of codes; boxes are 128 channels by:
 struct Maps {
   CUtensorMap gate, up;                      // CH rows, SK blocks: stored [block][row][128]
   CUtensorMap down[2];                       // a CTA's rows of W_down, by the parity of their count
@@ -89,10 +100,10 @@ struct Args {
   int reds;                 // buffers of units' sums
 };
 
-// R: token rows of an operand tile (T rounded up to 8).
 template <int N>
 using Int = std::integral_constant<int, N>;
 
+// R: token rows of an operand tile (T rounded up to 8).
 template <int R>
 struct Shape {
   static constexpr int N = SK * R;                          // MMA columns: token rows of the stage's two blocks

@@ -509,12 +509,12 @@ MOE_API int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int stream_i
 
 /*
  * ---------------------------------------------------------------- few tokens
- * moe_few_tokens: the whole layer for 1 <= T <= 16 tokens in one kernel (and
- * one small memset before it), for single-stream and small-batch decoding:
- * moe_route, moe_quant_1x128, the experts of moe_grouped_gemm_fp8 and
- * moe_combine ("DeepSeek-V3 Teknik Raporu", Yöntem 2 and Temel fikirler, FP8
- * bullet; the pages have no such kernel). Each touched expert's weights are
- * read once.
+ * moe_few_tokens: the whole layer for 1 <= T <= 16 tokens in two kernels (the
+ * router's affinities; everything behind them), for single-stream and
+ * small-batch decoding: moe_route, moe_quant_1x128, the experts of
+ * moe_grouped_gemm_fp8 and moe_combine ("DeepSeek-V3 Teknik Raporu", Yöntem 2
+ * and Temel fikirler, FP8 bullet; the pages have no such kernel). Each touched
+ * expert's weights are read once.
  *   u        [T][d] bf16: the router's input, and the experts' unless xq is given
  *   xq, xs   both NULL (u is quantised inside, bit for bit as moe_quant_1x128
  *            does), or the experts' input [T][d] E4M3, [T][d/128] FP32
@@ -527,14 +527,15 @@ MOE_API int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int stream_i
  *            expert's output to bf16 before the sum); may alias base or u
  *   topk_idx, gates  [T][K_r] int32, FP32 (out), ordered as moe_route orders them
  *   counts   NULL, or [N_r] int32 (out): tokens of each expert (moe_bias_update)
- *   workspace  moe_few_tokens_workspace(...) bytes, 16-byte aligned; its first
- *            bytes are zeroed by every call on its stream
+ *   workspace  moe_few_tokens_workspace(...) bytes, 16-byte aligned, of any
+ *            content
  * The logits are summed in FP64 and each affinity is rounded once to FP32, so
  * the selection is that of the exact affinities in FP32 keys; a NaN key sorts
- * below every other. The kernel is a cooperative launch of one CTA per SM: its
- * CTAs wait for one another, so two calls that share a workspace must not
- * overlap (calls with workspaces of their own may). Results do not depend on
- * the schedule. T = 0 only zeroes counts.
+ * below every other. The second kernel is a cooperative launch of one CTA per
+ * SM, whose CTAs wait for one another (bounded: MOE_ERR_TIMEOUT in the device
+ * error word). Two calls that share a workspace must not overlap; calls with
+ * workspaces of their own may. Results do not depend on the schedule, and a
+ * token's NaN or infinity reaches no other token. T = 0 only zeroes counts.
  * Limits: K_r <= 16, K_r <= N_r <= 256, d a multiple of 256 up to 8192 (and up
  * to 64 times the SM count), I a multiple of 128 up to 8192.
  * moe_few_tokens_workspace returns 0 for sizes outside the limits.
