@@ -407,8 +407,9 @@ def moe_bias_update(b, counts, T, K_r, gamma=0.001, max_over_mean=None, stream=N
         _stream(stream)))
 
 
-# The calls below are short (a few microseconds on the device), so their checks
-# are one expression a tensor; what fails it is named by the slow ones above.
+# The calls below take a few microseconds on the device, so what they cost on
+# the host counts: their checks are one expression a tensor, and what fails it
+# is named by the slow ones above.
 
 def _here(stream):
     """The current device, and the stream's handle (the current stream's by default)."""
@@ -416,12 +417,16 @@ def _here(stream):
     return dev, (torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
 
 
-def _p(t, dtype, shape, dev, name):
-    """The address of a checked tensor: dtype, shape, contiguous, on device dev."""
-    if t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
+def _refuse(t, dtype, shape, dev, name):
     _want(t, dtype, shape, name)
     raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+
+
+def _p(t, dtype, shape, dev, name):
+    """The address of a checked tensor: dtype, shape, contiguous, on device dev."""
+    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, dtype, shape, dev, name)
+    return t.data_ptr()
 
 
 def _popt(t, dtype, shape, dev, name):
@@ -432,10 +437,16 @@ def _ws(t, dev):
     """(address, bytes) of a workspace."""
     if t is None or not t.is_cuda or not t.is_contiguous() or t.get_device() != dev:
         raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{dev}")
-    return t.data_ptr(), t.numel() * t.element_size()
+    return t.data_ptr(), t.nbytes
 
 
-_FLOATS = (torch.bfloat16, torch.float32)
+def _done(call, status):
+    if status:
+        raise MoEError(call, status)
+
+
+_BF16, _FP32, _U8, _I32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+_FLOATS = (_BF16, _FP32)
 
 
 def moe_rmsnorm_quant(x, w, eps, y=None, q=None, scale=None, residual=None, h=None, stream=None):
@@ -443,20 +454,24 @@ def moe_rmsnorm_quant(x, w, eps, y=None, q=None, scale=None, residual=None, h=No
     as q and scale, in E4M3 1x128 tiles. x may be a column slice of a wider
     row-major tensor; residual and h are bf16 or FP32, w FP32 or bf16; outputs
     that are None are not written. h may be residual, y may be x."""
-    ld = _ld(x)
-    rows, d = x.shape
+    on = x.get_device()
+    if on < 0 or x.dim() != 2 or x.stride(1) != 1 or x.dtype is not _BF16:
+        raise ValueError("x must be a bf16 CUDA matrix with unit column stride")
     dev, handle = _here(stream)
-    if x.dtype is not torch.bfloat16 or x.get_device() != dev:
-        raise ValueError(f"x must be bf16 on cuda:{dev}")
-    st = residual.dtype if residual is not None else h.dtype if h is not None else torch.bfloat16
-    if st not in _FLOATS or w.dtype not in _FLOATS:
+    if on != dev:
+        raise ValueError(f"x is on {x.device}, but the current device is cuda:{dev}")
+    shape = x.shape
+    rows, d = shape
+    st = residual.dtype if residual is not None else h.dtype if h is not None else _BF16
+    wt = w.dtype
+    if st not in _FLOATS or wt not in _FLOATS:
         raise ValueError("residual, h and w must be bf16 or FP32")
-    bf, rd = torch.bfloat16, (rows, d)
-    check("moe_rmsnorm_quant", _lib.load().moe_rmsnorm_quant(
-        x.data_ptr(), ld if rows > 1 else d, _popt(residual, st, rd, dev, "residual"), st is torch.float32,
-        _p(w, w.dtype, (d,), dev, "w"), w.dtype is bf, eps, rows, d, _popt(h, st, rd, dev, "h"),
-        _popt(y, bf, rd, dev, "y"), _popt(q, torch.uint8, rd, dev, "q"),
-        _popt(scale, torch.float32, (rows, d // 128), dev, "scale"), handle))
+    _done("moe_rmsnorm_quant", _lib.load().moe_rmsnorm_quant(
+        x.data_ptr(), x.stride(0) if rows > 1 else d, None if residual is None else _p(residual, st, shape, dev, "residual"),
+        st is _FP32, _p(w, wt, (d,), dev, "w"), wt is _BF16, eps, rows, d,
+        None if h is None else _p(h, st, shape, dev, "h"), None if y is None else _p(y, _BF16, shape, dev, "y"),
+        None if q is None else _p(q, _U8, shape, dev, "q"),
+        None if scale is None else _p(scale, _FP32, (rows, d // 128), dev, "scale"), handle))
 
 
 def moe_rmsnorm_backward_workspace(rows, d):
@@ -468,15 +483,15 @@ def moe_rmsnorm_backward(dy, h, w, eps, dh, dw, workspace, dres=None, stream=Non
     one type (bf16 or FP32), dy is bf16, w FP32 or bf16. dh may be h or dres."""
     rows, d = h.shape
     dev, handle = _here(stream)
-    st = h.dtype
-    if st not in _FLOATS or w.dtype not in _FLOATS:
+    st, wt = h.dtype, w.dtype
+    if st not in _FLOATS or wt not in _FLOATS:
         raise ValueError("h and w must be bf16 or FP32")
     rd = (rows, d)
     ws, ws_bytes = _ws(workspace, dev)
-    check("moe_rmsnorm_backward", _lib.load().moe_rmsnorm_backward(
-        _p(dy, torch.bfloat16, rd, dev, "dy"), _p(h, st, rd, dev, "h"), st is torch.float32,
-        _p(w, w.dtype, (d,), dev, "w"), w.dtype is torch.bfloat16, eps, _popt(dres, st, rd, dev, "dres"), rows, d,
-        _p(dh, st, rd, dev, "dh"), _p(dw, torch.float32, (d,), dev, "dw"), ws, ws_bytes, handle))
+    _done("moe_rmsnorm_backward", _lib.load().moe_rmsnorm_backward(
+        _p(dy, _BF16, rd, dev, "dy"), _p(h, st, rd, dev, "h"), st is _FP32, _p(w, wt, (d,), dev, "w"), wt is _BF16, eps,
+        _popt(dres, st, rd, dev, "dres"), rows, d, _p(dh, st, rd, dev, "dh"), _p(dw, _FP32, (d,), dev, "dw"), ws,
+        ws_bytes, handle))
 
 
 def moe_few_tokens_workspace(T, d, N_r, K_r, I):
@@ -492,10 +507,10 @@ def moe_few_tokens(u, e, b, K_r, w_gate, w_up, w_down, s_gate, s_up, s_down, out
     N_r = b.shape[0]
     G, I = N_r + 1, w_gate.shape[1]
     dev, handle = _here(stream)
-    bf, f32, u8, i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+    bf, f32, u8, i32 = _BF16, _FP32, _U8, _I32
     td, tk, wi, si = (T, d), (T, K_r), (G, I, d), (G, I // 128, d // 128)
     ws, ws_bytes = _ws(workspace, dev)
-    check("moe_few_tokens", _lib.load().moe_few_tokens(
+    _done("moe_few_tokens", _lib.load().moe_few_tokens(
         _p(u, bf, td, dev, "u"), _popt(xq, u8, td, dev, "xq"), _popt(xs, f32, (T, d // 128), dev, "xs"),
         _popt(base, bf, td, dev, "base"), _p(e, bf, (N_r, d), dev, "e"), _p(b, f32, (N_r,), dev, "b"), T, d, N_r, K_r,
         _p(w_gate, u8, wi, dev, "w_gate"), _p(w_up, u8, wi, dev, "w_up"), _p(w_down, u8, (G, d, I), dev, "w_down"),

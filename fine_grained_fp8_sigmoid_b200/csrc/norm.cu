@@ -412,8 +412,9 @@ extern "C" int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int strea
     using S = decltype(s);
     using W = decltype(wt);
     auto k = rmsnorm_backward_kernel<S, W, decltype(n)::value>;
-    attr = cuda_status(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)),
-                       "rmsnorm backward: smem attribute");
+    if (smem > 40 * 1024)                                        // with the static part more than 48 KB need asking
+      attr = cuda_status(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)),
+                         "rmsnorm backward: smem attribute");
     if (attr == MOE_OK)
       k<<<parts, nt, smem, st_>>>(dy, static_cast<const S*>(h), static_cast<const W*>(w), eps, static_cast<const S*>(dres),
                                   rows, d, ring, static_cast<S*>(dh), part);

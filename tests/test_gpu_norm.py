@@ -160,7 +160,7 @@ def _check_backward(dy, h, w, eps, dres, dh, dw, rows):
 
 
 @pytest.mark.parametrize("rows,d", [(1, 128), (1, 7168), (2, 8), (37, 2048), (148, 256), (149, 256), (700, 384), (301, 7168),
-                                    (3, 16384), (1500, 72)])
+                                    (3, 16384), (1500, 72), (1900, 2048), (2500, 1024), (1200, 4096)])
 @pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32])
 def test_norm_backward(lib, rows, d, stream):
     from fine_grained_fp8_sigmoid_b200 import binding as B
