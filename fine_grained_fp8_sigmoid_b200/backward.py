@@ -34,6 +34,8 @@ class ExpertFFNBackward:
     def __init__(self, layer):
         self.layer = L = layer
         G, I, d = L.N_r + 1, L.I, L.d
+        if getattr(L, "few", False):
+            raise ValueError("the backward reads the separate steps' buffers: use a layer without few=True")
         if d % 256 or I % 256:
             raise ValueError("the backward's GEMMs need d and I multiples of 256")
         dev = dict(device=L.device)

@@ -230,13 +230,17 @@ class MoELayerFP8:
                     u_devs[(i + 1) % 2].copy_(u_hosts[i + 1], non_blocking=True)
                     h2d_done[(i + 1) % 2].record(copy)
             comp.wait_event(h2d_done[k])
-            self.route(u_devs[k], e, b)
-            self.quant(u_devs[k])
-            self.permute()
-            self.experts()
+            if not self.few:
+                self.route(u_devs[k], e, b)
+                self.quant(u_devs[k])
+                self.permute()
+                self.experts()
             if i >= 1:                    # batch i-1's h' has left self.out
                 comp.wait_event(d2h_done)
-            self.combine(u_devs[k])
+            if self.few:
+                self.few_tokens(u_devs[k], e, b)
+            else:
+                self.combine(u_devs[k])
             read_done[k].record(comp)
             out_ready.record(comp)
             if update_bias:

@@ -195,6 +195,15 @@ def test_largest_sizes(lib, T, d, I):
     check(p, o, exact=True)
 
 
+def test_full_shape(lib):
+    """Weights past 2^31 bytes a matrix."""
+    p = make(2, 7168, 256, 8, 2048, seed=2, integers=True)
+    o = buffers(p)
+    call(p, o)
+    no_error()
+    check(p, o, exact=True)
+
+
 def test_ties_go_to_the_lower_expert(lib):
     p = make(11, 512, 32, 5, 128, seed=4, integers=True)
     p["e"][1::2] = p["e"][0::2]          # pairs of equal centroids

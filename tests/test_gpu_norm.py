@@ -197,6 +197,29 @@ def test_norm_backward_of_no_rows_and_of_a_zero_row(lib):
     _check_backward(f64(dy), f64(h), f64(w), 1e-6, None, dh, dw, 4)
 
 
+def test_offsets_past_32_bits(lib):
+    from fine_grained_fp8_sigmoid_b200 import binding as B
+    rows, d = 140001, 16384
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.empty(rows, d, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    w = torch.ones(d, device="cuda")
+    y, q = torch.empty_like(x), torch.empty(rows, d, dtype=torch.uint8, device="cuda")
+    scale = torch.empty(rows, d // 128, device="cuda")
+    B.moe_rmsnorm_quant(x, w, 1e-6, y=y, q=q, scale=scale)
+    for at in (slice(0, 3), slice(131071, 131074), slice(rows - 3, rows)):     # rows * d is 2^31 at 131072
+        _check_forward(f64(x[at]), f64(w), 1e-6, None, y[at], q[at], scale[at])
+    dh, dw = torch.empty_like(x), torch.empty(d, device="cuda")
+    ws = torch.empty(B.moe_rmsnorm_backward_workspace(rows, d), dtype=torch.uint8, device="cuda")
+    del q, scale
+    B.moe_rmsnorm_backward(x, y, w, 1e-6, dh, dw, ws)
+    for at in (slice(0, 3), slice(131071, 131074), slice(rows - 3, rows)):
+        ref, _ = O.rmsnorm_backward(f64(x[at]), f64(y[at]), f64(w), 1e-6)
+        h, dy = f64(y[at]), f64(x[at])
+        r = 1.0 / np.sqrt((h ** 2).mean(-1, keepdims=True) + 1e-6)
+        terms = r * np.abs(dy) + r * np.abs(h * r) * np.abs(dy * h * r).mean(-1, keepdims=True)
+        assert (np.abs(f64(dh[at]) - ref) <= HALF[torch.bfloat16] * np.abs(ref) + 4 * ROUND * terms + TINY).all()
+
+
 def test_norm_and_gradient_replay_in_a_graph(lib):
     from fine_grained_fp8_sigmoid_b200 import binding as B
     rows, d = 200, 1024

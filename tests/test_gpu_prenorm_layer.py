@@ -123,6 +123,22 @@ def test_forward_with_few_tokens_without_a_norm(lib):
     assert (err <= 2 * bound + 2.0 ** -8 * y + 2.0 ** -7 * (ref.to(D).abs() + 2 * bound)).all()
 
 
+def test_few_tokens_from_host_batches(lib):
+    """The pipelined host path of a few-token layer runs the few-token calls."""
+    cfg = workloads.CONFIGS["tiny"].with_tokens(7)
+    layer = _layer(cfg, few=True)
+    e, b = workloads.centroids(cfg).cuda(), workloads.bias(cfg).cuda()
+    g = torch.Generator().manual_seed(2)
+    us = [torch.randn(cfg.T, cfg.d, generator=g).to(torch.bfloat16).pin_memory() for _ in range(5)]
+    outs = [torch.empty_like(u).pin_memory() for u in us]
+    devs = [torch.empty(cfg.T, cfg.d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    layer.forward_host_pipelined(us, e, b, outs, devs, update_bias=False)
+    torch.cuda.synchronize()
+    for u, o in zip(us, outs):
+        assert torch.equal(layer.forward(u.cuda(), e, b, update_bias=False).cpu(), o)
+    no_error()
+
+
 def test_gradient_of_the_norm_behind_the_experts(lib):
     from fine_grained_fp8_sigmoid_b200.backward import ExpertFFNBackward
     cfg = workloads.CONFIGS["mid"].with_tokens(96)
@@ -149,3 +165,5 @@ def test_layer_refusals(lib):
         layer.forward_prenorm(x, torch.ones(256, device="cuda"), None, None)
     with pytest.raises(ValueError, match="prenorm=True"):
         ExpertFFNBackward(layer).norm_backward(x, torch.ones(256, device="cuda"))
+    with pytest.raises(ValueError, match="few=True"):
+        ExpertFFNBackward(MoELayerFP8(4, 256, 8, 2, 256, few=True))
