@@ -389,13 +389,19 @@ __device__ __forceinline__ void select_token(const Args& a, int t, float* score,
 
 // Every CTA selects for itself (scores: CW * MAX_N floats of scratch): slot 0 is the shared expert with every token,
 // then the touched experts in ascending order, their tokens ascending.
+// A warp selects for R / CW tokens: code runs once and cold here, so there is
+// no more of it than the tokens need.
+template <int R>
 __device__ __forceinline__ void select_all(const Args& a, Small* sm, float* scores) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int ex[2] = {0, 0};
-  float g[2] = {0.0f, 0.0f};
+  constexpr int PER = R / CW;
+  int ex[PER];
+  float g[PER];
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
+  for (int r = 0; r < PER; ++r) {
     const int t = warp + r * CW;
+    ex[r] = 0;
+    g[r] = 0.0f;
     if (t >= a.T) continue;
     select_token(a, t, scores + warp * MAX_N, ex[r], g[r]);
     if (lane < a.K) atomicOr(&sm->mask[ex[r]], 1u << t);
@@ -437,7 +443,7 @@ __device__ __forceinline__ void select_all(const Args& a, Small* sm, float* scor
     sm->ent_gate[lane] = 1.0f;
   }
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
+  for (int r = 0; r < PER; ++r) {
     const int t = warp + r * CW;
     if (t < a.T && lane < a.K) {
       const int p = sm->slot_start[sm->slot_of[ex[r]]] + __popc(sm->mask[ex[r]] & ((1u << t) - 1u));
@@ -636,7 +642,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
   } else {
     // ------------------------------------------------------------ selection
     const int tid = threadIdx.x;
-    select_all(a, sm, red);
+    select_all<R>(a, sm, red);
     named_bar_sync(1, CW * 32);
     const int slots = sm->n_slots, units = slots * per;
 
