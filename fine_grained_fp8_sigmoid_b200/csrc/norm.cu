@@ -8,20 +8,38 @@ namespace norm {
 
 // Eight consecutive values as FP32: bf16 (one 16-byte access) or FP32 (two).
 // Plain loads, not the read-only path: outputs may alias inputs.
-__device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+template <typename T>
+struct Raw8;                                 // as loaded: what is still on its way
+template <>
+struct Raw8<uint16_t> {
+  uint4 v;
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
   }
-}
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p);
-  const float4 b = *reinterpret_cast<const float4*>(p + 4);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+};
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
+  Raw8<T> r;
+  r.load(p);
+  r.get(f);
 }
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return float_to_bf16_bits(lo) | (static_cast<uint32_t>(float_to_bf16_bits(hi)) << 16);
@@ -99,13 +117,15 @@ __device__ __forceinline__ void store_codes(const float (&t)[8], bool on, uint8_
 // One row per blockDim.x threads, VPT runs of 8 channels a thread, held in
 // registers between the sum of squares and the outputs: every input is read
 // once and every output written once. Memory bounds it: T = 8192, d = 7168 with
-// a bf16 residual moves 530 MB in 100 us (5.3 of the copy's 6.45 TB/s; 56% of
-// the bytes are writes, and without the codes' arithmetic it takes 98 us).
-// A block per row beats blocks that stay and fetch the next row ahead, into
-// registers (108 us) or by bulk copies into a ring (106 us): enough rows are in
-// flight on an SM, and their waits overlap. 224 threads a row (four runs each)
-// beat 448 (125 us). With at most a row per SM the row's latency counts, and a
-// thread takes one run.
+// a bf16 residual moves 530 MB in 88 us, 6.0 of the copy's 6.45 TB/s. What
+// carries it is that x and res are all on their way before the first is used
+// (100 us with a load per use: stores and loads that may alias keep their
+// order) and that many rows share an SM, whose waits overlap: a block per row
+// beats blocks that stay and fetch the next row ahead, into registers (108 us
+// against 100) or by bulk copies into a ring (106), and w is loaded late, which
+// costs a wait and spares the registers of a fourth block (102 us with w loaded
+// at once after the sum). With at most a row per SM the row's latency counts,
+// and a thread takes one run.
 template <typename S, typename W, int VPT>
 __global__ void __launch_bounds__(1024) rmsnorm_quant_kernel(const uint16_t* x, long long ldx, const S* res,
                                                              const W* w, float eps, int rows, int d, S* h,
@@ -117,19 +137,30 @@ __global__ void __launch_bounds__(1024) rmsnorm_quant_kernel(const uint16_t* x, 
   const size_t base = static_cast<size_t>(live ? row : 0) * d;
   float s[VPT][8];
   float ss[1] = {0.0f};
+  Raw8<uint16_t> xr[VPT];                    // all loads before the first use
+  Raw8<S> rr[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
     if (live && v < V) {
-      load8(x + static_cast<size_t>(row) * ldx + v * 8, s[i]);
+      xr[i].load(x + static_cast<size_t>(row) * ldx + v * 8);
+      if (res != nullptr) rr[i].load(res + base + v * 8);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    if (live && v < V) {
+      xr[i].get(s[i]);
       if (res != nullptr) {
         float r[8];
-        load8(res + base + v * 8, r);
+        rr[i].get(r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) s[i][j] += r[j];
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss[0] = fmaf(s[i][j], s[i][j], ss[0]);
+      if (h != nullptr) store8(h + base + v * 8, s[i]);
     }
   }
   row_sum(ss, red_all + threadIdx.y * 32);
@@ -140,7 +171,6 @@ __global__ void __launch_bounds__(1024) rmsnorm_quant_kernel(const uint16_t* x, 
     const bool on = live && v < V;
     float t[8];
     if (on) {
-      if (h != nullptr) store8(h + base + v * 8, s[i]);
       load8(w + v * 8, t);
 #pragma unroll
       for (int j = 0; j < 8; ++j) t[j] *= s[i][j] * rstd;
