@@ -128,7 +128,8 @@ __device__ __forceinline__ void store_codes(const float (&t)[8], bool on, uint8_
 // and a thread takes one run.
 template <typename S, typename W, int VPT>
 __global__ void __launch_bounds__(1024) rmsnorm_quant_kernel(const uint16_t* x, long long ldx, const S* res,
-                                                             const W* w, float eps, int rows, int d, S* h,
+                                                             const W* w, float eps, float inv_d, int rows, int d,
+                                                             S* h,
                                                              uint16_t* y, uint8_t* q, float* scale) {
   __shared__ float red_all[4 * 32];
   const int row = blockIdx.x * blockDim.y + threadIdx.y;
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_quant_kernel(const uint16_t* x, 
     }
   }
   row_sum(ss, red_all + threadIdx.y * 32);
-  const float rstd = __frsqrt_rn(ss[0] / static_cast<float>(d) + eps);
+  const float rstd = rsqrtf(fmaf(ss[0], inv_d, eps));
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
@@ -181,25 +182,25 @@ __global__ void __launch_bounds__(1024) rmsnorm_quant_kernel(const uint16_t* x, 
   }
 }
 
-// Sums two values over the `warps` warps of a block's rows; every thread gets
-// the sums. red: 64 floats, of a pair that the next call does not use.
+// Sums two values over the `warps` (at most 16) first warps of a block; every
+// thread gets the sums. The lower half of a warp sums the first value and the
+// upper half the second: 11 shuffles in place of 20. red: 32 floats that the
+// next call does not use.
 __device__ __forceinline__ void block_sum2(float& a, float& b, float* red, int warps) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
-  }
-  if (warps == 1) return;
   const int warp = threadIdx.x >> 5, lane = lane_id();
-  if (lane == 0) { red[warp] = a; red[32 + warp] = b; }
-  named_bar_sync(1, warps * 32);
-  a = lane < warps ? red[lane] : 0.0f;
-  b = lane < warps ? red[32 + lane] : 0.0f;
+  const bool up = lane >= 16;
+  float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (warps > 1) {
+    if ((lane & 15) == 0) red[lane + warp] = v;          // the first value's 16 places, then the second's
+    named_bar_sync(1, warps * 32);
+    v = (lane & 15) < warps ? red[lane] : 0.0f;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   }
+  a = __shfl_sync(0xffffffffu, v, 0);
+  b = __shfl_sync(0xffffffffu, v, 16);
 }
 
 __device__ __forceinline__ void bulk_row(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -216,17 +217,17 @@ constexpr int MAX_RING = 8;
 // partial row it writes. The last warp keeps a ring of whole rows (h, dy, dres)
 // on their way into shared memory by bulk copies: a row is used twice with a
 // sum over the block between, and with plain loads the block stood still for
-// their latency twice a row. T = 8192, d = 7168: 82 us with the column sums
-// (470 MB, 5.7 TB/s) against 247 with plain loads; 4096 x 2048 in FP32: 25 us,
+// their latency twice a row. T = 8192, d = 7168: 79 us with the column sums
+// (470 MB, 6.0 TB/s) against 247 with plain loads; 4096 x 2048 in FP32: 25 us,
 // where half of the issue slots are taken and the sums over a row's warps cost
 // as much as its arithmetic.
 template <typename S, typename W, int VPT>
-__global__ void __launch_bounds__(544) rmsnorm_backward_kernel(const uint16_t* dy, const S* h, const W* w, float eps,
+__global__ void __launch_bounds__(544) rmsnorm_backward_kernel(const uint16_t* dy, const S* h, const W* w, float eps, float inv_d,
                                                                const S* dres, int rows, int d, int ring, S* dh,
                                                                float* part) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint64_t full[MAX_RING], empty[MAX_RING];
-  __shared__ float red_all[2][64];
+  __shared__ float red_all[2][32];
   __shared__ int abort_flag;
   volatile int* abort = &abort_flag;
   const int warps = (blockDim.x >> 5) - 1, warp = threadIdx.x >> 5;
@@ -288,8 +289,8 @@ __global__ void __launch_bounds__(544) rmsnorm_backward_kernel(const uint16_t* d
         }
       }
       block_sum2(hh, gh, red_all[flip], warps);
-      const float r = __frsqrt_rn(hh / static_cast<float>(d) + eps);
-      const float c = gh / static_cast<float>(d) * r * r;
+      const float r = rsqrtf(fmaf(hh, inv_d, eps));
+      const float c = gh * inv_d * r * r;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int v = threadIdx.x + i * warps * 32;
@@ -382,7 +383,8 @@ extern "C" int moe_rmsnorm_quant(const uint16_t* x, long long ldx, const void* r
     using S = decltype(s);
     using W = decltype(wt);
     rmsnorm_quant_kernel<S, W, decltype(n)::value><<<grid, block, 0, as_stream(stream)>>>(
-        x, ldx, static_cast<const S*>(res), static_cast<const W*>(w), eps, rows, d, static_cast<S*>(h), y, q, scale);
+        x, ldx, static_cast<const S*>(res), static_cast<const W*>(w), eps, 1.0f / d, rows, d,
+        static_cast<S*>(h), y, q, scale);
   };
   auto by_vpt = [&](auto s, auto wt) {
     if (vpt == 1) launch(s, wt, std::integral_constant<int, 1>{});
@@ -420,8 +422,8 @@ extern "C" int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int strea
   DeviceInfo di;
   if (int st = device_info(&di)) return st;
   const int V = d / 8;
-  // Threads a row, measured at 8192 rows: 256 channels of 8 take 36 us with 128 threads and four blocks an SM, 39
-  // with 256 and three; 896 take 82 us with 224 threads and two blocks, 107 with 448 and one.
+  // Threads a row, measured at 8192 rows: 256 runs of 8 channels took 36 us with 128 threads and four blocks an SM,
+  // 39 with 256 and three; 896 took 82 us with 224 threads and two blocks, 107 with 448 and one.
   const int vpt = vpt_for(V, V <= 256 ? 128 : V <= 1024 ? 256 : 512);
   const int nt = ((V + vpt - 1) / vpt + 31) / 32 * 32 + 32;      // and the copying warp
   const size_t row_bytes = static_cast<size_t>(d) * (2 + (stream_is_fp32 ? 4 : 2) * (dres ? 2 : 1));
@@ -446,7 +448,7 @@ extern "C" int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int strea
       attr = cuda_status(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)),
                          "rmsnorm backward: smem attribute");
     if (attr == MOE_OK)
-      k<<<parts, nt, smem, st_>>>(dy, static_cast<const S*>(h), static_cast<const W*>(w), eps, static_cast<const S*>(dres),
+      k<<<parts, nt, smem, st_>>>(dy, static_cast<const S*>(h), static_cast<const W*>(w), eps, 1.0f / d, static_cast<const S*>(dres),
                                   rows, d, ring, static_cast<S*>(dh), part);
   };
   auto by_vpt = [&](auto s, auto wt) {

@@ -2,8 +2,10 @@
 
 Tolerances. All sums and products are FP32. s = x + res is one rounding; its
 squares are non-negative, so their sum (at most 32 values a thread in order,
-then 5 + 32 exchanged) is off by at most 70 roundings, which the square root
-halves; y takes four more. That is under ROUND = 64 steps of 2^-24 relative.
+then 5 + 32 exchanged) is off by at most 70 roundings, its mean by three more
+(1/d, the product, eps), which the square root halves; the root itself is
+good to two units (4 steps of 2^-24), and y takes three more. That is under
+ROUND = 64 steps of 2^-24 relative.
 Stored values add half a step of their type. dh adds three terms, each off by
 ROUND + the 70 of the projection; dw adds over rows in order.
 """
