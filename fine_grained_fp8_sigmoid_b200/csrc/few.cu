@@ -355,6 +355,7 @@ __device__ __forceinline__ uint32_t ordered(float k) {
 // the warp's own.
 __device__ __forceinline__ void select_token(const Args& a, int t, float* score, int& ex, float& s) {
   const int lane = lane_id();
+  __syncwarp();                              // the scratch's last token has been read
   uint32_t key[MAX_N / 32];
 #pragma unroll
   for (int j = 0; j < MAX_N / 32; ++j) {
