@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* part, int
 
 constexpr int MAX_D = 1024 * 8 * 4;
 constexpr int BWD_MAX_D = 512 * 8 * 4;
+constexpr int BWD_MAX_ROWS = 1 << 30;         // a block's row, stepped past the last one, stays in 32 bits
 constexpr int MAX_PARTS = 592;
 
 inline int vpt_for(int V, int threads) {
@@ -408,7 +409,7 @@ extern "C" int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int strea
   using namespace moe;
   using namespace moe::norm;
   MOE_CHECK_ARG(rows >= 0 && d >= 0 && eps >= 0.0f);
-  MOE_CHECK_SUPPORTED(d % 8 == 0 && d <= BWD_MAX_D);
+  MOE_CHECK_SUPPORTED(d % 8 == 0 && d <= BWD_MAX_D && rows <= BWD_MAX_ROWS);
   if (d == 0) return MOE_OK;
   MOE_CHECK_ARG(dw);
   cudaStream_t st_ = as_stream(stream);

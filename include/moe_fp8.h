@@ -499,7 +499,7 @@ MOE_API int moe_rmsnorm_quant(const uint16_t* x, long long ldx, const void* res,
  *   dw     [d] FP32 (out)
  *   workspace  moe_rmsnorm_backward_workspace(rows, d) bytes, 16-byte aligned
  * Sums are FP32 in an order that the sizes alone fix: no atomics. rows = 0
- * gives dw = 0. Limits: d a multiple of 8, at most 16384.
+ * gives dw = 0. Limits: d a multiple of 8, at most 16384; rows at most 2^30.
  */
 MOE_API size_t moe_rmsnorm_backward_workspace(int rows, int d);
 MOE_API int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int stream_is_fp32,

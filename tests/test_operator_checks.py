@@ -73,6 +73,16 @@ def test_norm_refusals():
     assert back(rows=-2) == INV and back(eps=-1.0) == INV
 
 
+def test_norm_backward_refuses_rows_past_2_to_the_30():
+    lib = _lib.load()
+    A, N = ctypes.c_void_p(1 << 20), None    # an address that is never read
+    size = lib.moe_rmsnorm_backward_workspace(2**31 - 1, 8)
+    assert size == lib.moe_rmsnorm_backward_workspace(1 << 30, 8)
+    for rows in ((1 << 30) + 1, 2**31 - 1):
+        assert lib.moe_rmsnorm_backward(A, A, 0, A, 0, ctypes.c_float(1e-6), N, rows, 8, A, A, A, size,
+                                        ctypes.c_void_p(0)) == _lib.MOE_ERR_UNSUPPORTED
+
+
 def test_few_tokens_refusals():
     lib = _lib.load()
     N, s = None, ctypes.c_void_p(0)
