@@ -919,15 +919,10 @@ inline Layout layout(int T, int d, int N_r, int K_r, int I) {
 
 // [rows][cols] codes as (128, rows, cols / 128), boxes of CH rows by SK blocks.
 inline int make_map(CUtensorMap* m, const void* base, size_t rows, int cols) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return record_failure(MOE_ERR_CUDA, "cuTensorMapEncodeTiled", "entry point not found");
-  cuuint64_t dims[3] = {128, rows, static_cast<cuuint64_t>(cols / 128)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols), 128};
-  cuuint32_t box[3] = {128, CH, SK}, one[3] = {1, 1, 1};
-  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, one,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? MOE_OK : record_failure(MOE_ERR_CUDA, "cuTensorMapEncodeTiled", "few tokens: weight map");
+  const cuuint64_t dims[3] = {128, rows, static_cast<cuuint64_t>(cols / 128)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols), 128};
+  const cuuint32_t box[3] = {128, CH, SK};
+  return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box);
 }
 
 template <int R>

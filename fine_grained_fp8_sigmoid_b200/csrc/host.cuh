@@ -82,31 +82,48 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
+// Encodes a map of `rank` dimensions, innermost first, with the 128-byte swizzle;
+// out-of-range boxes are zero-filled. The driver's call wants a context that is
+// current in the calling host thread, and a thread whose first CUDA work this is
+// has none yet: the current device's is then made current and the call repeated.
+inline int encode_tmap(CUtensorMap* m, CUtensorMapDataType dtype, int rank, const void* base, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return record_failure(MOE_ERR_CUDA, "cuTensorMapEncodeTiled", "entry point not found");
+  const cuuint32_t estr[3] = {1, 1, 1};
+  auto call = [&] {
+    return enc(m, dtype, rank, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = call();
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return cuda_status(e, "tensor map: current device");
+    r = call();
+  }
+  if (r != CUDA_SUCCESS) {
+    char what[128];
+    snprintf(what, sizeof what, "CUresult %d (dims %llu x %llu, box %u x %u)", static_cast<int>(r),
+             static_cast<unsigned long long>(dims[0]), static_cast<unsigned long long>(dims[1]), box[0], box[1]);
+    return record_failure(MOE_ERR_CUDA, "cuTensorMapEncodeTiled", what);
+  }
+  return MOE_OK;
+}
+
 // 2-D row-major tensor [rows][cols] of `elem_bytes`-byte elements, copied in
 // boxes of box_rows x box_cols with the 128-byte swizzle (box_cols *
 // elem_bytes must be 128). Out-of-range boxes are zero-filled.
 inline int make_tmap_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dtype,
                         int elem_bytes, uint64_t rows, uint64_t cols, uint32_t box_rows,
                         uint32_t box_cols) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return record_failure(MOE_ERR_CUDA, "cuTensorMapEncodeTiled", "entry point not found");
   if (reinterpret_cast<uintptr_t>(base) % 16 != 0) return MOE_ERR_INVALID_ARG;
   if ((cols * elem_bytes) % 16 != 0) return MOE_ERR_UNSUPPORTED;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * static_cast<cuuint64_t>(elem_bytes)};
-  cuuint32_t box[2] = {box_cols, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(m, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) {
-    char what[96];
-    snprintf(what, sizeof what, "CUresult %d (rows %llu, cols %llu, box %ux%u)", static_cast<int>(r),
-             static_cast<unsigned long long>(rows), static_cast<unsigned long long>(cols), box_rows,
-             box_cols);
-    return record_failure(MOE_ERR_CUDA, "cuTensorMapEncodeTiled", what);
-  }
-  return MOE_OK;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {cols * static_cast<cuuint64_t>(elem_bytes)};
+  const cuuint32_t box[2] = {box_cols, box_rows};
+  return encode_tmap(m, dtype, 2, base, dims, strides, box);
 }
 
 }  // namespace moe
