@@ -948,7 +948,9 @@ int launch(const Maps& maps, Args& a, int G, cudaStream_t s) {
   static_assert(MAX_STAGES % MI == 0 && BUFS % MI == 0, "stages and buffers are dealt to the issuers");
   const size_t smem = rest + static_cast<size_t>(a.stages) * STAGE;
   auto k = few_tokens_kernel<R>;
-  if (int st = cuda_status(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)),
+  // the limit belongs to the function, not to the launch: one value for every shape, so that a call of another host
+  // thread cannot lower it before this launch
+  if (int st = cuda_status(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX),
                            "few tokens: smem attribute"))
     return st;
   cudaLaunchConfig_t cfg = {};

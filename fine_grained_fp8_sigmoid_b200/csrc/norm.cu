@@ -349,6 +349,7 @@ constexpr int MAX_D = 1024 * 8 * 4;
 constexpr int BWD_MAX_D = 512 * 8 * 4;
 constexpr int BWD_MAX_ROWS = 1 << 30;         // a block's row, stepped past the last one, stays in 32 bits
 constexpr int MAX_PARTS = 592;
+constexpr int BWD_SMEM = 220 * 1024;          // of an SM's 227 KB, for the rings of its blocks
 
 inline int vpt_for(int V, int threads) {
   int vpt = 1;
@@ -430,7 +431,7 @@ extern "C" int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int strea
   const size_t row_bytes = static_cast<size_t>(d) * (2 + (stream_is_fp32 ? 4 : 2) * (dres ? 2 : 1));
   int per_sm = nt <= 160 ? 4 : nt <= 288 && row_bytes <= 36 * 1024 ? 3 : row_bytes <= 54 * 1024 ? 2 : 1;
   if (rows <= di.sm_count) per_sm = 1;
-  int ring = static_cast<int>(220 * 1024 / per_sm / row_bytes);
+  int ring = static_cast<int>(BWD_SMEM / per_sm / row_bytes);
   if (ring > MAX_RING) ring = MAX_RING;
   if (ring < 1) ring = 1;
   int parts = di.sm_count * per_sm;
@@ -445,8 +446,10 @@ extern "C" int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int strea
     using S = decltype(s);
     using W = decltype(wt);
     auto k = rmsnorm_backward_kernel<S, W, decltype(n)::value>;
-    if (smem > 40 * 1024)                                        // with the static part more than 48 KB need asking
-      attr = cuda_status(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)),
+    // With the static part more than 48 KB need asking. The limit belongs to the function, not to the launch: one value
+    // for every shape, so that a call of another host thread cannot lower it before this launch.
+    if (smem > 40 * 1024)
+      attr = cuda_status(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, BWD_SMEM),
                          "rmsnorm backward: smem attribute");
     if (attr == MOE_OK)
       k<<<parts, nt, smem, st_>>>(dy, static_cast<const S*>(h), static_cast<const W*>(w), eps, 1.0f / d, static_cast<const S*>(dres),
