@@ -31,8 +31,11 @@ inline int record_failure(int status, const char* where, const char* what) {
   return status;
 }
 
+// A runtime call that fails also leaves its error behind, for the thread's next
+// launch_status to find: it is taken along here, so that it fails no later call.
 inline int cuda_status(cudaError_t e, const char* where) {
   if (e == cudaSuccess) return MOE_OK;
+  cudaGetLastError();
   return record_failure(MOE_ERR_CUDA, where, cudaGetErrorString(e));
 }
 
