@@ -100,6 +100,22 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
+// Waits for what a block still has in flight (copies into its shared memory,
+// MMAs on its TMEM) before it ends. Those finish by themselves, so this wait
+// goes on where the block's other roles have given up; it has a limit of its own.
+__device__ __forceinline__ bool mbar_drain(uint64_t* bar, uint32_t parity) {
+  constexpr uint64_t limit_ns = 100000000ull;
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((n & 63) == 0 && globaltimer_ns() - t0 > limit_ns) {
+      set_device_error(MOE_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
 // ---------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* m) {

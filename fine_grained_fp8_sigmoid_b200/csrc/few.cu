@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
       }
       // no copy may be in flight when the CTA ends
       for (int j = max(0, issued - a.stages); j < issued; ++j)
-        if (j % MI == warp - CW) mbar_wait(&sm->full[j % a.stages], (j / a.stages) & 1, abort);
+        if (j % MI == warp - CW) mbar_drain(&sm->full[j % a.stages], (j / a.stages) & 1);
     }
   } else if (warp >= CW + MI) {
     // ------------------------------------------------------------ MMA issuers (the whole warp keeps step)
@@ -636,8 +636,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
       }
     }
     if (lane == 0) {
-      umma_commit(&sm->drained);                // no MMA may run when the TMEM is freed
-      mbar_wait(&sm->drained, 0, abort);
+      umma_commit(&sm->drained);                // no MMA may run when the TMEM is freed, and the tokens' codes have landed
+      mbar_drain(&sm->drained, 0);
+      mbar_drain(&sm->x_ready, 0);
     }
     __syncwarp();
   } else {
@@ -882,7 +883,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const __grid_con
           bulk_load(hb + kb_i * tile_bytes, a.hs + first * a.hs_pitch, ntok * a.hs_pitch * 4, &sm->hfull[h.i]);
         h.next(a.hbufs);
       }
-      for (int j = max(0, n - a.hbufs); j < n; ++j) mbar_wait(&sm->hfull[j % a.hbufs], (j / a.hbufs) & 1, abort);
+      for (int j = max(0, n - a.hbufs); j < n; ++j) mbar_drain(&sm->hfull[j % a.hbufs], (j / a.hbufs) & 1);
     }
   }
   tc_fence_before();

@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(544) rmsnorm_backward_kernel(const uint16_t* d
         if (dres != nullptr) bulk_row(dst + hb + yb, dres + base, hb, &full[s]);
         if (++s == ring) { s = 0; lap ^= 1; }
       }
-      for (int j = max(0, n - ring); j < n; ++j) mbar_wait(&full[j % ring], (j / ring) & 1, abort);
+      for (int j = max(0, n - ring); j < n; ++j) mbar_drain(&full[j % ring], (j / ring) & 1);
     }
   } else {
     const int V = d >> 3;
