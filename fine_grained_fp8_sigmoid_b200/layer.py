@@ -44,6 +44,9 @@ class MoELayerFP8:
                  fuse_quant=False, few=False, prenorm=False):
         if few and T > 16:
             raise ValueError("few=True is for at most 16 tokens")
+        if few and not B.moe_few_tokens_workspace(max(T, 1), d, N_r, K_r, I):
+            raise ValueError("few=True needs 1 <= K_r <= 16, K_r <= N_r <= 256, d a multiple of 256 and I a multiple "
+                             "of 128, both at most 8192")
         self.T, self.d, self.N_r, self.K_r, self.I = T, d, N_r, K_r, I
         self.fuse_quant = bool(fuse_quant)
         self.gather = (T * K_r <= 64 * N_r) if gather is None else bool(gather)
