@@ -89,7 +89,10 @@ class MoELayerFP8:
         """Views of the last step's expert intermediate H in the GEMM
         workspace (the layout include/moe_fp8.h gives for
         moe_grouped_gemm_fp8): E4M3 codes [T*K_r + T][I] (routed rows in
-        permuted order, then the T shared rows) and their FP32 1x128 scales."""
+        permuted order, then the T shared rows) and their FP32 1x128 scales.
+        A few-token layer's forward keeps no such rows."""
+        if self.few:
+            raise ValueError("a layer with few=True keeps no intermediate: use one without it")
         rows, I = self.T * self.K_r + self.T, self.I
         off = (rows * I + 255) // 256 * 256
         codes = self.ws_gemm[:rows * I].view(rows, I)

@@ -21,3 +21,12 @@ def test_sizes_outside_the_limits_are_refused_before_any_allocation(monkeypatch,
 @pytest.mark.parametrize("T", [0, 1, 16])
 def test_sizes_inside_the_limits_are_not(T):
     assert MoELayerFP8(T, 256, 8, 8, 128, device="cpu", few=True).ws_few is not None
+
+
+def test_there_is_no_intermediate_to_view():
+    """Its forward does not write the grouped GEMM's workspace: the views would hold whatever was there."""
+    layer = MoELayerFP8(2, 256, 8, 2, 128, device="cpu", few=True)
+    with pytest.raises(ValueError, match="few=True"):
+        layer.intermediate()
+    codes, scales = MoELayerFP8(2, 256, 8, 2, 128, device="cpu").intermediate()
+    assert codes.shape == (6, 128) and scales.shape == (6, 1)
