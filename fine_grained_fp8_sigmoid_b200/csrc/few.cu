@@ -25,13 +25,15 @@
 // in the last round), and in the second phase a CTA has its own d / SMs rows of
 // W_down, at most 64, over all slots.
 //
-// Measured back to back (d = 7168, I = 2048, 8 of 256 experts and the shared
-// one; weights alone take 61 / 216 / 704 us at the copy rate of 6.45 TB/s): one
-// token 75 us, of them 4 for the first kernel; 4 tokens 234 to 242 us; 16
-// tokens 713 to 790 us. DRAM bounds them; at one token the starts of the two
-// kernels and the selection (about 13 us) come on top. With small experts
-// (d = 2048, I = 1024, 6 of 64) one token takes 25 us against 7: the exchange
-// between the phases is six round trips through a loaded L2.
+// Measured from a graph of calls over three sets of inputs (d = 7168, I = 2048,
+// 8 of 256 experts and the shared one; weights alone take 61 / 216 / 704 us at
+// the copy rate of 6.45 TB/s): one token 75 us, of them 4 for the first kernel;
+// 4 tokens 230 to 242 us; 16 tokens 713 to 820 us, by the machine and from run
+// to run. A call by itself through the binding takes 79 us at one token. DRAM
+// bounds them; at one token the starts of the two kernels and the selection
+// (about 13 us) come on top. With small experts (d = 2048, I = 1024, 6 of 64)
+// one token takes 26 us against 7: the exchange between the phases is six round
+// trips through a loaded L2.
 #include "host.cuh"
 
 namespace moe {

@@ -117,8 +117,10 @@ __device__ __forceinline__ void store_codes(const float (&t)[8], bool on, uint8_
 // One row per blockDim.x threads, VPT runs of 8 channels a thread, held in
 // registers between the sum of squares and the outputs: every input is read
 // once and every output written once. Memory bounds it: T = 8192, d = 7168 with
-// a bf16 residual moves 530 MB in 88 us, 6.0 of the copy's 6.45 TB/s. What
-// carries it is that x and res are all on their way before the first is used
+// a bf16 residual moves 530 MB in 88 us, 6.0 of the copy's 6.45 TB/s (events
+// around one call behind a read of 256 MB, as all figures here; 86 us from a
+// graph of calls, 92 to 95 as calls one after the other through the binding,
+// each behind the last one's writes). What carries it is that x and res are all on their way before the first is used
 // (100 us with a load per use: stores and loads that may alias keep their
 // order) and that many rows share an SM, whose waits overlap: a block per row
 // beats blocks that stay and fetch the next row ahead, into registers (108 us
@@ -218,7 +220,8 @@ constexpr int MAX_RING = 8;
 // on their way into shared memory by bulk copies: a row is used twice with a
 // sum over the block between, and with plain loads the block stood still for
 // their latency twice a row. T = 8192, d = 7168: 79 us with the column sums
-// (470 MB, 6.0 TB/s) against 247 with plain loads; 4096 x 2048 in FP32: 25 us,
+// (470 MB, 6.0 TB/s; events around one call, 75 us from a graph, 80 to 84 as
+// calls one after the other) against 247 with plain loads; 4096 x 2048 in FP32: 25 us,
 // where half of the issue slots are taken and the sums over a row's warps cost
 // as much as its arithmetic.
 template <typename S, typename W, int VPT>
@@ -425,7 +428,8 @@ extern "C" int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int strea
   if (int st = device_info(&di)) return st;
   const int V = d / 8;
   // Threads a row, measured at 8192 rows: 256 runs of 8 channels took 36 us with 128 threads and four blocks an SM,
-  // 39 with 256 and three; 896 took 82 us with 224 threads and two blocks, 107 with 448 and one.
+  // 39 with 256 and three; 896 took 82 us with 224 threads and two blocks, 107 with 448 and one (33 and 79
+  // of the ones taken since a row's two sums share an exchange).
   const int vpt = vpt_for(V, V <= 256 ? 128 : V <= 1024 ? 256 : 512);
   const int nt = ((V + vpt - 1) / vpt + 31) / 32 * 32 + 32;      // and the copying warp
   const size_t row_bytes = static_cast<size_t>(d) * (2 + (stream_is_fp32 ? 4 : 2) * (dres ? 2 : 1));

@@ -35,7 +35,13 @@ class MoELayerFP8:
 
     few=True (T <= 16) runs forward as moe_few_tokens: the whole layer in two
     kernels, each touched expert's weights read once, expert outputs summed in
-    FP32 (the separate steps round them to bf16 first).
+    FP32 (the separate steps round them to bf16 first). Its router sums logits
+    in FP64 and moe_route in FP32, so where keys lie within FP32's error of one
+    another the two forms of the layer may select different experts. gather and
+    fuse_quant concern the separate steps alone, which remain callable one by
+    one; forward then writes out, topk_idx, gates and counts, and neither the
+    permutation nor y_perm, y_shared and the intermediate (xq and xs only in
+    forward_prenorm).
 
     prenorm=True adds the buffers of forward_prenorm: h, the residual stream
     after the addition, and u, its root-mean-square norm."""

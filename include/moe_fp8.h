@@ -498,8 +498,10 @@ MOE_API int moe_rmsnorm_quant(const uint16_t* x, long long ldx, const void* res,
  *   dh     [rows][d] of h's type (out); may alias dres or h
  *   dw     [d] FP32 (out)
  *   workspace  moe_rmsnorm_backward_workspace(rows, d) bytes, 16-byte aligned
- * Sums are FP32 in an order that the sizes alone fix: no atomics. rows = 0
- * gives dw = 0. Limits: d a multiple of 8, at most 16384; rows at most 2^30.
+ * Sums are FP32 without atomics, in an order that rows, d, the stream's type,
+ * whether dres is given and the device's SM count fix: a call repeats itself
+ * bit for bit, and dw with and without dres may differ in the order of its
+ * sums. rows = 0 gives dw = 0. Limits: d a multiple of 8, at most 16384; rows at most 2^30.
  */
 MOE_API size_t moe_rmsnorm_backward_workspace(int rows, int d);
 MOE_API int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int stream_is_fp32,
@@ -535,7 +537,8 @@ MOE_API int moe_rmsnorm_backward(const uint16_t* dy, const void* h, int stream_i
  * SM, whose CTAs wait for one another (bounded: MOE_ERR_TIMEOUT in the device
  * error word). Two calls that share a workspace must not overlap; calls with
  * workspaces of their own may. Results do not depend on the schedule, and a
- * token's NaN or infinity reaches no other token. T = 0 only zeroes counts.
+ * token's NaN or infinity reaches no other token; which experts the other
+ * tokens select can change the order in which a token's FP32 sum is formed. T = 0 only zeroes counts.
  * Limits: K_r <= 16, K_r <= N_r <= 256, d a multiple of 256 up to 8192 (and up
  * to 64 times the SM count), I a multiple of 128 up to 8192.
  * moe_few_tokens_workspace returns 0 for sizes outside the limits.
